@@ -7,6 +7,7 @@ raises when the library is missing, and every call raises on a non-zero status.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -41,6 +42,11 @@ SIGNATURES = {
     "cp_merge_partials": (_I, [_I, _I64, _I, _P, _P, _P, _P, _P]),
     "cp_layout_permute": (_I, [_P, _I, _P, _P, _I, _P]),
     "cp_rope_permute": (_I, [_P, _P, _P, ctypes.c_double, _I64, _P]),
+    "cp_rope_axes_permute": (_I, [_P, _I, _P, _P, _P, _I, _P, ctypes.c_double, _I, _I, _P]),
+    "cp_linattn_fwd": (_I, [_P] * 10),
+    "cp_linattn_bwd": (_I, [_P] * 14),
+    "cp_linattn_workspace_bytes": (_SZ, [_P]),
+    "cp_linattn_step": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _F, _P, _P, _P]),
     "cp_layout_index_map_len": (_I64, [_P]),
     "cp_layout_index_map": (_I, [_P, _P, _P]),
     "cp_attn_check": (_I, [_P, _P]),
@@ -107,6 +113,11 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _device(index):
+    """Context with that device current (nothing without one)."""
+    return contextlib.nullcontext() if index is None else torch.cuda.device(index)
+
+
 class Plan:
     """A context-parallel attention plan (wraps ``cp_attn_plan``)."""
 
@@ -115,6 +126,8 @@ class Plan:
         self.B, self.H, self.S, self.D, self.N = B, H, S, D, N
         self.causal, self.layout = bool(causal), layout
         self.scale = softmax_scale if softmax_scale > 0 else 1.0 / math.sqrt(D)
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else None
+        self._linattn_ws = None
         h = ctypes.c_void_p()
         _check("cp_attn_plan", lib().cp_attn_plan(ctypes.byref(h), B, H, S, D, N, int(bool(causal)),
                                                    LAYOUTS[layout], float(softmax_scale)))
@@ -191,6 +204,12 @@ class Plan:
         rows = [tuple(items[5 * i:5 * i + 5]) for i in range(n)]
         n_cta = max(r[4] for r in rows) + 1 if rows else 0
         return rows, list(loads)[:n_cta]
+
+    def linattn_workspace_bytes(self) -> int:
+        if self._linattn_ws is None:
+            with _device(self.device):
+                self._linattn_ws = int(lib().cp_linattn_workspace_bytes(self._h))
+        return self._linattn_ws
 
     def workspace_bytes(self, with_partials: bool = False) -> int:
         return int(lib().cp_attn_workspace_bytes(self._h, int(with_partials)))
@@ -399,6 +418,173 @@ def rope_permute(plan: Plan, x, out=None, base: float = 10000.0, pos_offset: int
     _check("cp_rope_permute", lib().cp_rope_permute(plan.handle, _ptr(x), _ptr(out), float(base), int(pos_offset),
                                                     _stream(stream)))
     return out
+
+
+ROPE_FREQS = {"shared": 0, "per_axis": 1}
+ROPE_PAIRINGS = {"adjacent": 0, "half": 1}
+
+
+def _expect(name, t, dtype, shape, device):
+    """Raise ValueError unless ``t`` is a contiguous tensor of that type and shape on ``device``."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _enqueue(device, stream, body):
+    """``body(stream pointer)`` with ``device`` current. What it allocates belongs to the
+    stream it launches on, so a temporary freed on return is not reused too early."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return body(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return body(torch.cuda.current_stream().cuda_stream)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _shapes(plan: Plan):
+    """(natural or Ulysses-shard shape, attention input shape) of the plan's tensors."""
+    B, H, S, D, N = plan.B, plan.H, plan.S, plan.D, plan.N
+    if plan.layout == "ulysses":
+        return (N, B, S // N, H, D), (N, B, S, H // N, D)
+    return (B, S, H, D), (N, B, S // N, H, D)
+
+
+def rope_axes(plan: Plan, x, positions, sections, base: float = 10000.0, freqs: str = "shared",
+              pairing: str = "adjacent", inverse: bool = False, out=None, stream=None):
+    """``cp_rope_axes_permute``: rotary embedding with one position per axis, fused into
+    the forward layout map; ``inverse`` is its gradient (inverse rotation and map).
+
+    x: bf16, natural [B, S, H, D] (Ulysses: shards [N, B, S/N, H, D]), or, with
+    ``inverse``, in the attention input layout. positions: int32 [axes, B, S], natural
+    token order. sections: feature pairs of each axis, their sum D/2. freqs: "shared"
+    (base^(-2i/D) over all pairs) or "per_axis" (base^(-j/n) within each axis's n
+    pairs). pairing: "adjacent" (2i, 2i+1) or "half" (i, i + D/2). Returns the rotated
+    tensor in the other layout."""
+    src, dst = _shapes(plan)
+    if inverse:
+        src, dst = dst, src
+    dev = x.device
+    _expect("x", x, torch.bfloat16, src, dev)
+    sections = [int(n) for n in sections]
+    _expect("positions", positions, torch.int32, (len(sections), plan.B, plan.S), dev)
+    if freqs not in ROPE_FREQS or pairing not in ROPE_PAIRINGS:
+        raise ValueError(f"freqs must be one of {sorted(ROPE_FREQS)}, pairing one of {sorted(ROPE_PAIRINGS)}")
+    if out is not None:
+        _expect("out", out, torch.bfloat16, dst, dev)
+    sec = (ctypes.c_int * max(len(sections), 1))(*sections)
+
+    def body(s):
+        y = torch.empty(dst, dtype=torch.bfloat16, device=dev) if out is None else out
+        _check("cp_rope_axes_permute",
+               lib().cp_rope_axes_permute(plan.handle, int(bool(inverse)), x.data_ptr(), y.data_ptr(),
+                                          positions.data_ptr(), len(sections), sec, float(base), ROPE_FREQS[freqs],
+                                          ROPE_PAIRINGS[pairing], s))
+        return y
+
+    return _enqueue(dev, stream, body)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _linattn_inputs(plan, log_decay, states, **tensors):
+    shape = _shapes(plan)[1]
+    dev = tensors["q"].device
+    for name, t in tensors.items():
+        if t is not None:
+            _expect(name, t, torch.bfloat16, shape, dev)
+    _expect("log_decay", log_decay, torch.float32, (plan.H,), dev)
+    for name, t in states.items():
+        if t is not None:
+            _expect(name, t, torch.float32, (plan.B, plan.H, plan.D, plan.D), dev)
+    return shape, dev
+
+
+def _linattn_workspace(plan, workspace, dev):
+    n = plan.linattn_workspace_bytes()
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev) if n > 0 else None
+    if workspace.device != dev or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < n:
+        raise ValueError(f"workspace: expected {n} contiguous bytes on {dev}")
+    return workspace
+
+
+def linattn_fwd(plan: Plan, q, k, v, log_decay, state_in=None, want_state: bool = False, o=None, state_out=None,
+                workspace=None, stream=None):
+    """``cp_linattn_fwd``: causal linear attention with a decay exp(log_decay[h]) per head.
+
+    q, k, v: bf16 in the plan's layout [N, B, S/N, H, D] (a causal contiguous or zigzag
+    plan); log_decay: fp32 [H], <= 0; state_in: fp32 [B, H, D, D] or None. Returns
+    (o, state after the last token, or None unless ``want_state`` or given)."""
+    shape, dev = _linattn_inputs(plan, log_decay, {"state_in": state_in, "state_out": state_out}, q=q, k=k, v=v, o=o)
+
+    def body(s):
+        y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if o is None else o
+        z = state_out
+        if z is None and want_state:
+            z = torch.empty(plan.B, plan.H, plan.D, plan.D, dtype=torch.float32, device=dev)
+        ws = _linattn_workspace(plan, workspace, dev)
+        _check("cp_linattn_fwd",
+               lib().cp_linattn_fwd(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                    _opt(state_in), y.data_ptr(), _opt(z), _opt(ws), s))
+        return y, z
+
+    return _enqueue(dev, stream, body)
+
+
+def linattn_bwd(plan: Plan, q, k, v, log_decay, dout, state_in=None, dstate_out=None, want_dstate: bool = False,
+                dq=None, dk=None, dv=None, dstate_in=None, workspace=None, stream=None):
+    """``cp_linattn_bwd``: gradients (dq, dk, dv, dstate_in) of ``linattn_fwd``; dstate_in
+    is None unless ``want_dstate`` or given. dstate_out: gradient of the state after the
+    last token, or None."""
+    shape, dev = _linattn_inputs(plan, log_decay,
+                                 {"state_in": state_in, "dstate_out": dstate_out, "dstate_in": dstate_in},
+                                 q=q, k=k, v=v, dout=dout, dq=dq, dk=dk, dv=dv)
+
+    def body(s):
+        g = [torch.empty(shape, dtype=torch.bfloat16, device=dev) if t is None else t for t in (dq, dk, dv)]
+        z = dstate_in
+        if z is None and want_dstate:
+            z = torch.empty(plan.B, plan.H, plan.D, plan.D, dtype=torch.float32, device=dev)
+        ws = _linattn_workspace(plan, workspace, dev)
+        _check("cp_linattn_bwd",
+               lib().cp_linattn_bwd(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                    dout.data_ptr(), _opt(state_in), _opt(dstate_out), g[0].data_ptr(),
+                                    g[1].data_ptr(), g[2].data_ptr(), _opt(z), _opt(ws), s))
+        return g[0], g[1], g[2], z
+
+    return _enqueue(dev, stream, body)
+
+
+def linattn_step(q, k, v, log_decay, state, scale: float = 0.0, o=None, stream=None):
+    """``cp_linattn_step``: the recurrent form on T <= 16 new tokens, q, k, v bf16
+    [B, T, H, D]; ``state`` (fp32 [B, H, D, D]) is updated in place. scale 0 selects
+    1/sqrt(D). Returns o."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, T, H, D], got {tuple(q.shape)}")
+    B, T, H, D = q.shape
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+        if t is not None:
+            _expect(name, t, torch.bfloat16, q.shape, dev)
+    _expect("log_decay", log_decay, torch.float32, (H,), dev)
+    _expect("state", state, torch.float32, (B, H, D, D), dev)
+
+    def body(s):
+        y = torch.empty_like(q) if o is None else o
+        _check("cp_linattn_step",
+               lib().cp_linattn_step(B, T, H, D, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                     scale if scale > 0 else 1.0 / math.sqrt(D), state.data_ptr(), y.data_ptr(), s))
+        return y
+
+    return _enqueue(dev, stream, body)
 
 
 def attn_bwd(plan: Plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, workspace=None, stream=None):

@@ -18,6 +18,7 @@
 #include "sp_norm.h"
 #include "cp_attn.h"
 #include "geometry.h"
+#include "plan_view.h"
 
 using namespace cpattn;
 
@@ -90,7 +91,6 @@ struct cp_attn_plan_s {
 
 namespace {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s per in-kernel wait
 constexpr int64_t kPullChunkBytes = 32768;          // fused-pull copy unit
 constexpr int kDefaultSmCount = kDefaultSmCountPlan;
 
@@ -309,6 +309,14 @@ int ensure_device(cp_attn_plan_s* p) {
   return CP_ERR_CUDA;
 }
 
+// A launch on the plan goes to the device that holds its tables: the one it was made on.
+int on_plan_device(const cp_attn_plan_s* p) {
+  if (p->d_status == nullptr) return CP_ERR_CUDA;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CP_ERR_CUDA;
+  return dev == p->device ? CP_OK : CP_ERR_INVALID_ARG;
+}
+
 // First step of the tail phase of a one-launch ring forward: half the steps run
 // one unit per step, the rest in one unit per query-tile pair.
 int ring_split(int nr) { return nr <= 2 ? nr : (nr + 1) / 2; }
@@ -475,6 +483,33 @@ PermuteArgs permute_args(const cp_attn_plan_s* p, int direction, int elem_bytes)
 }
 
 }  // namespace
+
+namespace cpattn {
+
+int plan_view(const cp_attn_plan_s* plan, PlanView* out) {
+  const int rc = on_plan_device(plan);
+  if (rc != CP_OK) return rc;
+  *out = PlanView{plan->B,      plan->H,     plan->S,   plan->D,       plan->N, plan->causal,
+                  plan->layout, plan->scale, plan->sms, plan->d_status};
+  return CP_OK;
+}
+
+bool encode_map_4d(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t d3, int box1,
+                   int box2) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2),
+                              static_cast<cuuint64_t>(d3)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d0) * 2, static_cast<cuuint64_t>(d0) * d1 * 2,
+                                 static_cast<cuuint64_t>(d0) * d1 * d2 * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace cpattn
 
 extern "C" {
 
@@ -1029,6 +1064,40 @@ int cp_rope_permute(cp_attn_plan_t plan, const void* in, void* out, double base,
   ra.pos_offset = pos_offset;
   ra.D = plan->D;
   return launch_rope_permute(permute_args(plan, 0, 2), ra, in, out, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* in, void* out, const int32_t* positions,
+                         int axes, const int* sections, double base, int freqs, int pairing, cp_stream_t stream) {
+  if (plan == nullptr || in == nullptr || out == nullptr || positions == nullptr || sections == nullptr)
+    return CP_ERR_INVALID_ARG;
+  if (direction != 0 && direction != 1) return CP_ERR_INVALID_ARG;
+  if (freqs != CP_ROPE_FREQS_SHARED && freqs != CP_ROPE_FREQS_PER_AXIS) return CP_ERR_INVALID_ARG;
+  if (pairing != CP_ROPE_PAIRS_ADJACENT && pairing != CP_ROPE_PAIRS_HALF) return CP_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base)) return CP_ERR_INVALID_ARG;
+  const int D = plan->D;
+  if (axes < 1 || axes > D / 2) return CP_ERR_INVALID_ARG;
+  RopeAxesArgs ra;
+  std::memset(&ra, 0, sizeof(ra));
+  int pair = 0;
+  for (int x = 0; x < axes; ++x) {
+    const int n = sections[x];
+    if (n < 1 || n > D / 2 - pair) return CP_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j, ++pair) {
+      ra.axis[pair] = static_cast<unsigned char>(x);
+      ra.theta[pair] = std::pow(base, freqs == CP_ROPE_FREQS_PER_AXIS ? -static_cast<double>(j) / n : -2.0 * pair / D);
+    }
+  }
+  if (pair != D / 2) return CP_ERR_INVALID_ARG;
+  if (!aligned16(in) || !aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return CP_ERR_ALIGNMENT;
+  const int rc = on_plan_device(plan);
+  if (rc != CP_OK) return rc;
+  ra.axis_stride = static_cast<int64_t>(plan->B) * plan->S;
+  ra.inverse = direction;
+  ra.half = pairing == CP_ROPE_PAIRS_HALF;
+  return launch_rope_axes(permute_args(plan, direction, 2), ra, positions, in, out,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? CP_OK
              : CP_ERR_CUDA;
 }

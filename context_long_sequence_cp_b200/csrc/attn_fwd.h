@@ -96,6 +96,18 @@ struct RopeArgs {
 cudaError_t launch_rope_permute(const PermuteArgs& a, const RopeArgs& ra, const void* in, void* out,
                                 cudaStream_t stream);
 
+// Rotary embedding over several position axes: per feature pair its frequency
+// (fp64) and its axis; positions[axis * axis_stride + natural flat token].
+struct RopeAxesArgs {
+  double theta[64];
+  int64_t axis_stride;   // B * S
+  unsigned char axis[64];
+  int inverse;           // 1: rotate by the negative angle
+  int half;              // 1: pairs (i, i + D/2), 0: pairs (2i, 2i + 1)
+};
+cudaError_t launch_rope_axes(const PermuteArgs& a, const RopeAxesArgs& ra, const int* positions, const void* in,
+                             void* out, cudaStream_t stream);
+
 // merge_permute.cu: the bounded-wait self-test (a wait on a barrier nothing arrives on)
 cudaError_t launch_wait_probe(int* status, uint64_t limit_ns, cudaStream_t stream);
 

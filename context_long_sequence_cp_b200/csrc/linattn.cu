@@ -1,0 +1,764 @@
+// linattn.cu — causal linear attention with a decay for each head (sm_100a,
+// tcgen05 + TMEM + TMA), its gradients, and its recurrent form.
+//
+//   S_t = d S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   d = exp(log_decay[h]).
+//
+// One engine computes the output and every gradient. For rows a, b, c and a state Z0,
+//   y_i = s_in sum_{j<=i} d^(i-j) (a_i . b_j) c_j + s_st d^(i+e) a_i^T Z0
+// in one direction over the tokens:
+//   o  : a, b, c = q, k, v     Z0 = S_0      e = 1   forward
+//   dq : a, b, c = do, v, k    Z0 = S_0^T    e = 1   forward
+//   dk : a, b, c = v, do, q    Z0 = dS_T^T   e = 0   backward over the tokens
+//   dv : a, b, c = k, q, do    Z0 = dS_T     e = 0   backward; its final state is dS_0
+// (sum_i d^(i+1) scale q_i do_i^T + d^S dS_T).
+//
+// Chunked form, chunks of 128 tokens (never across a rank's piece). With Z the state
+// before a chunk of L tokens and p the row's index in walking order:
+//   Y  = ((A B^T) o M) C + diag(d^(p+e)) A Z,   M_pj = d^(p-j) for j <= p,
+//   Z' = d^L Z + B^T diag(d^(L-1-p+1-e)) C.
+// Four products on the tensor core per chunk; the chunk's decay mask is built from 32
+// powers of d and three row factors, so no exponential is taken per score.
+//
+// A CTA owns 64 columns of C (and of Z) of one (batch, head) and walks a run of
+// chunks ("segment"); Z stays in the registers of one warpgroup in fp32. Sequences with
+// few (batch, head) are cut into segments: a first launch (OUT = false) computes each
+// segment's own state, and the second joins those before it at its start.
+//
+// Precision. The state is exact to fp32: the weighted rows of C are split into three
+// bf16 terms (8 + 8 + 8 bits of the fp32 product) that are multiplied side by side as
+// one N = 192 operand and summed smallest first; the chunk sum starts from zero in TMEM
+// and is added to d^L Z in registers, d^L as an fp32 pair, because the tensor core's
+// accumulation truncates and a long run of it would drift. Rounded to bf16: the masked
+// scores (P), and the state where it is multiplied by A (Z); both once, as operands.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "cp_attn.h"
+#include "linattn.h"
+#include "plan_view.h"
+#include "sm100.cuh"
+
+namespace cpattn {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kChunk = 128;     // tokens of a chunk: the 128 lanes of a tcgen05 product
+constexpr int kSlice = 64;      // columns of C and Z per CTA
+constexpr int kBlk = kChunk * 128;   // 128 rows x 128 B: one swizzled 64-column block
+
+template <int D, bool OUT>
+struct LinCfg {
+  static constexpr int kWide = kChunk * D * 2;            // a 128 x D tile
+  static constexpr int kStageBytes = (OUT ? 2 : 1) * kWide + kBlk;
+  static constexpr int kStages = OUT ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 4);
+  static constexpr int kThreads = OUT ? 448 : 320;
+  static constexpr int kMmaWarp = OUT ? 12 : 8;
+  // TMEM columns: chunk state [0,192), and with OUT the scores/P [192,320),
+  // A Z [320,384), P C [384,448).
+  static constexpr int kTmemCols = OUT ? 512 : 256;
+};
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);    // A B^T
+constexpr uint32_t kIdescKV = idesc_bf16_f32(128, 192, 1, 1);   // B^T C (both MN-major)
+constexpr uint32_t kIdescY = idesc_bf16_f32(128, 64, 0, 1);     // A Z, P C
+
+template <int D, bool OUT>
+struct alignas(1024) LinSmem {
+  // Stage: [A tile] B tile, C slice. For D = 64 the state product's upper 64 rows
+  // (unused) read the block after B, which is the C slice.
+  uint8_t stage[LinCfg<D, OUT>::kStages][LinCfg<D, OUT>::kStageBytes];
+  uint8_t cs[3][kBlk];                    // weighted C: high, middle, low terms
+  uint8_t z[OUT ? D * 128 : 16];          // bf16 state, row = feature of A
+  uint64_t full[LinCfg<D, OUT>::kStages], empty[LinCfg<D, OUT>::kStages];
+  uint64_t s_full, p_ready, cs_ready, kv_done, zq_done, z_ready, y_full, y_free, drain;
+  float pow32[32];                        // d^0 .. d^31
+  uint32_t tmem_base;
+  WaitBlock wblk;
+};
+static_assert(sizeof(LinSmem<128, true>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, true>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<128, false>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+
+// d^n; n = 0 gives 1 also for d = 0.
+__device__ __forceinline__ double decay_pow(double ld, int64_t n) {
+  return n == 0 ? 1.0 : exp(ld * static_cast<double>(n));
+}
+
+// Chunk ci in walking order: where its rows are.
+struct ChunkAt {
+  int rank, t0, len;
+  int before;   // tokens walked before it
+};
+__device__ __forceinline__ ChunkAt chunk_at(const LinParams& p, int ci) {
+  const int cn = p.reverse ? p.nch - 1 - ci : ci;
+  const int piece = cn / p.chunks_per_piece;
+  const int off = (cn - piece * p.chunks_per_piece) * kChunk;
+  ChunkAt c;
+  c.len = min(kChunk, p.piece_len - off);
+  if (!p.zigzag) {
+    c.rank = piece;
+    c.t0 = off;
+  } else {
+    c.rank = piece < p.N ? piece : 2 * p.N - 1 - piece;
+    c.t0 = (piece < p.N ? 0 : p.piece_len) + off;
+  }
+  const int p0 = piece * p.piece_len + off;
+  c.before = p.reverse ? p.S - p0 - c.len : p0;
+  return c;
+}
+__device__ __forceinline__ int walked_before(const LinParams& p, int ci) {
+  return ci >= p.nch ? p.S : chunk_at(p, ci).before;
+}
+
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+template <int D, bool OUT>
+__global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
+    linattn_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ LinParams p) {
+  using C = LinCfg<D, OUT>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  LinSmem<D, OUT>& sm = *reinterpret_cast<LinSmem<D, OUT>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  constexpr int kSlices = D / kSlice;
+  const int unit = static_cast<int>(blockIdx.x) % p.units;
+  const int seg = static_cast<int>(blockIdx.x) / p.units;
+  const int slice = unit % kSlices;
+  const int bh = unit / kSlices;
+  const int h = bh % p.H, b = bh / p.H;
+  const int ci0 = static_cast<int>(static_cast<int64_t>(seg) * p.nch / p.nseg);
+  const int ci1 = static_cast<int>(static_cast<int64_t>(seg + 1) * p.nch / p.nseg);
+  const int n = ci1 - ci0;
+  const double ld = static_cast<double>(__ldg(p.log_decay + h));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_addr(&sm.full[s]), 1);
+      mbar_init(smem_addr(&sm.empty[s]), 1);
+    }
+    mbar_init(smem_addr(&sm.s_full), 1);
+    mbar_init(smem_addr(&sm.p_ready), 128);
+    mbar_init(smem_addr(&sm.cs_ready), 128);
+    mbar_init(smem_addr(&sm.kv_done), 1);
+    mbar_init(smem_addr(&sm.zq_done), 1);
+    mbar_init(smem_addr(&sm.z_ready), 128);
+    mbar_init(smem_addr(&sm.y_full), 1);
+    mbar_init(smem_addr(&sm.y_free), 128);
+    mbar_init(smem_addr(&sm.drain), 1);
+    wait_block_init(sm.wblk, p.status, p.wait_limit_ns);
+    fence_barrier_init();
+  }
+  if (threadIdx.x < 32) sm.pow32[threadIdx.x] = static_cast<float>(decay_pow(ld, threadIdx.x));
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(smem_addr(&sm.tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == C::kMmaWarp + 1 && lane == 0) {
+    prefetch_tensormap(&tm_a);
+    prefetch_tensormap(&tm_b);
+    prefetch_tensormap(&tm_c);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const WaitCtl ctl = wait_ctl(sm.wblk);
+  constexpr uint32_t kOffB = OUT ? C::kWide : 0, kOffC = kOffB + C::kWide;
+  const uint32_t tS = tbase + 192, tAZ = tbase + 320, tPC = tbase + 384;
+
+  if (warp == C::kMmaWarp + 1) {
+    // ---------------------------------------------------------------- TMA
+    const uint64_t pol = l2_policy_evict_first();
+    bool ok = true;
+    int i = 0;
+    for (; i < n; ++i) {
+      const int st = i % NS;
+      if (i >= NS) ok = all_ok(mbar_wait(smem_addr(&sm.empty[st]), (i / NS - 1) & 1, ctl));
+      if (!ok) break;
+      const ChunkAt c = chunk_at(p, ci0 + i);
+      const uint32_t bar = smem_addr(&sm.full[st]);
+      const uint32_t dst = smem_addr(&sm.stage[st][0]);
+      const int rb = c.rank * p.B + b;
+      mbar_arrive_expect_tx_elect(bar, C::kStageBytes);
+      for (int blk = 0; blk < kSlices; ++blk)
+        tma_load_4d_elect(dst + kOffB + blk * kBlk, &tm_b, bar, blk * 64, h, c.t0, rb, pol);
+      tma_load_4d_elect(dst + kOffC, &tm_c, bar, slice * 64, h, c.t0, rb, pol);
+      if constexpr (OUT)
+        for (int blk = 0; blk < kSlices; ++blk)
+          tma_load_4d_elect(dst + blk * kBlk, &tm_a, bar, blk * 64, h, c.t0, rb, pol);
+    }
+    if (!ok)   // abort: let every load this warp issued land before the CTA exits
+      for (int k = i - NS; k < i; ++k)
+        if (k >= 0) mbar_wait_drain(smem_addr(&sm.full[k % NS]), (k / NS) & 1, p.wait_limit_ns);
+  } else if (warp == C::kMmaWarp) {
+    // ---------------------------------------------------------------- MMA
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % NS;
+      const uint32_t base = smem_addr(&sm.stage[st][0]);
+      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.full[st]), (i / NS) & 1, ctl)))) break;
+      tc_fence_after();
+      if constexpr (OUT) {
+        // Scores. P of the previous chunk shares the columns: its product was issued before.
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
+          umma_ss_elect(tS, smem_desc_sw128(base + off, 16, 1024), smem_desc_sw128(base + kOffB + off, 16, 1024),
+                        kIdescS, kk > 0);
+        }
+        umma_commit_elect(smem_addr(&sm.s_full));
+      }
+      // Chunk state: its TMEM columns are free once the state warpgroup has read the
+      // previous chunk's (with OUT it then also published the state before this chunk).
+      if (OUT || i > 0)
+        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.z_ready), (OUT ? i : i - 1) & 1, ctl)))) break;
+      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.cs_ready), i & 1, ctl)))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kChunk / 16; ++kk)
+        umma_ss_elect(tbase, smem_desc_sw128(base + kOffB + kk * 2048, kBlk, 1024),
+                      smem_desc_sw128(smem_addr(&sm.cs[0][0]) + kk * 2048, kBlk, 1024), kIdescKV, kk > 0);
+      umma_commit_elect(smem_addr(&sm.kv_done));
+      if constexpr (OUT) {
+        if (i > 0)
+          if (!(ok = all_ok(mbar_wait(smem_addr(&sm.y_free), (i - 1) & 1, ctl)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_elect(tAZ, smem_desc_sw128(base + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024),
+                        smem_desc_sw128(smem_addr(&sm.z[0]) + kk * 2048, kBlk, 1024), kIdescY, kk > 0);
+        umma_commit_elect(smem_addr(&sm.zq_done));
+        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.p_ready), i & 1, ctl)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          umma_ts_elect(tPC, tS + kk * 8, smem_desc_sw128(base + kOffC + kk * 2048, kBlk, 1024), kIdescY, kk > 0);
+        umma_commit_elect(smem_addr(&sm.y_full));
+      }
+      umma_commit_elect(smem_addr(&sm.empty[st]));
+    }
+    if (n > 0) {   // every product and commit has to finish before TMEM is freed
+      umma_commit_elect(smem_addr(&sm.drain));
+      mbar_wait_drain(smem_addr(&sm.drain), 0, p.wait_limit_ns);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------- weighted C, in three bf16 terms
+    const int row = threadIdx.x;
+    float w_full = 0.f;
+    {
+      const int x = p.reverse ? row + 1 : kChunk - 1 - row;
+      w_full = static_cast<float>(decay_pow(ld, x)) * p.s_upd;
+    }
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % NS;
+      const ChunkAt c = chunk_at(p, ci0 + i);
+      float w = w_full;
+      if (!p.reverse && c.len < kChunk && row < c.len)
+        w = static_cast<float>(decay_pow(ld, c.len - 1 - row)) * p.s_upd;
+      const bool live = row < c.len;
+      ok = all_ok(mbar_wait(smem_addr(&sm.full[st]), (i / NS) & 1, ctl));
+      if (ok && i > 0) ok = all_ok(mbar_wait(smem_addr(&sm.kv_done), (i - 1) & 1, ctl));
+      if (!ok) break;
+      const uint8_t* src = &sm.stage[st][kOffC] + row * 128;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = (j ^ (row & 7)) * 16;   // 128-byte swizzle of the 16-byte vector
+        const uint4 v = *reinterpret_cast<const uint4*>(src + at);
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t t0[4], t1[4], t2[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x0 = live ? __uint_as_float(in[q] << 16) * w : 0.f;
+          const float x1 = live ? __uint_as_float(in[q] & 0xffff0000u) * w : 0.f;
+          t0[q] = pack_bf16x2(x0, x1);
+          const float r0 = x0 - __uint_as_float(t0[q] << 16), r1 = x1 - __uint_as_float(t0[q] & 0xffff0000u);
+          t1[q] = pack_bf16x2(r0, r1);
+          t2[q] = pack_bf16x2(r0 - __uint_as_float(t1[q] << 16), r1 - __uint_as_float(t1[q] & 0xffff0000u));
+        }
+        const int dst = row * 128 + at;
+        *reinterpret_cast<uint4*>(&sm.cs[0][dst]) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+        *reinterpret_cast<uint4*>(&sm.cs[1][dst]) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        *reinterpret_cast<uint4*>(&sm.cs[2][dst]) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(smem_addr(&sm.cs_ready));
+    }
+  } else if (warp < 8) {
+    // --------------------------------------------------------- state, one row per lane
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;        // feature of B (row of Z)
+    const bool live = row < D;
+    const uint32_t tKV = tbase + (static_cast<uint32_t>(quad * 32) << 16);
+    float z[kSlice];
+#pragma unroll
+    for (int q = 0; q < kSlice; ++q) z[q] = 0.f;
+    const int64_t state0 = static_cast<int64_t>(bh) * D * D;
+    if (OUT && live) {
+      const int x = walked_before(p, ci0);
+      if (p.z0 != nullptr) {
+        const float w = static_cast<float>(decay_pow(ld, x));
+#pragma unroll
+        for (int q = 0; q < kSlice; ++q) {
+          const int col = slice * kSlice + q;
+          const int64_t at = p.z0_transposed ? static_cast<int64_t>(col) * D + row : static_cast<int64_t>(row) * D + col;
+          z[q] = w * __ldg(p.z0 + state0 + at);
+        }
+      }
+      for (int g = 0; g < seg; ++g) {
+        const int end = walked_before(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
+        const float w = static_cast<float>(decay_pow(ld, x - end));
+        const float4* src = reinterpret_cast<const float4*>(
+            p.zseg + ((static_cast<int64_t>(unit) * (p.nseg - 1) + g) * D + row) * kSlice);
+#pragma unroll
+        for (int q = 0; q < kSlice / 4; ++q) {
+          const float4 v = src[q];
+          z[4 * q] = fmaf(w, v.x, z[4 * q]);
+          z[4 * q + 1] = fmaf(w, v.y, z[4 * q + 1]);
+          z[4 * q + 2] = fmaf(w, v.z, z[4 * q + 2]);
+          z[4 * q + 3] = fmaf(w, v.w, z[4 * q + 3]);
+        }
+      }
+    }
+    auto publish = [&]() {   // bf16 state for A Z
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(&sm.z[row * 128 + ((j ^ (row & 7)) * 16)]) =
+              make_uint4(pack_bf16x2(z[8 * j], z[8 * j + 1]), pack_bf16x2(z[8 * j + 2], z[8 * j + 3]),
+                         pack_bf16x2(z[8 * j + 4], z[8 * j + 5]), pack_bf16x2(z[8 * j + 6], z[8 * j + 7]));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    };
+    if constexpr (OUT) {
+      publish();
+      mbar_arrive(smem_addr(&sm.z_ready));
+    }
+    const double dfull = decay_pow(ld, kChunk);
+    const int tail = p.piece_len % kChunk;
+    const double dtail = decay_pow(ld, tail);
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const ChunkAt c = chunk_at(p, ci0 + i);
+      const double dl = c.len == kChunk ? dfull : dtail;
+      const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
+      if (!(ok = all_ok(mbar_wait(smem_addr(OUT ? &sm.zq_done : &sm.kv_done), i & 1, ctl)))) break;
+      tc_fence_after();
+      if (quad * 32 < D) {
+#pragma unroll
+        for (int q = 0; q < kSlice; q += 16) {
+          uint32_t t0[16], t1[16], t2[16];
+          tmem_ld16(tKV + q, t0);
+          tmem_ld16(tKV + 64 + q, t1);
+          tmem_ld16(tKV + 128 + q, t2);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float sum = __uint_as_float(t0[k]) + (__uint_as_float(t1[k]) + __uint_as_float(t2[k]));
+            z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, sum));
+          }
+        }
+      }
+      tc_fence_before();
+      if (OUT && i + 1 < n) publish();
+      if (i + 1 < n) mbar_arrive(smem_addr(&sm.z_ready));
+    }
+    if (ok && live) {
+      float* dst = nullptr;
+      if (OUT) {
+        if (seg == p.nseg - 1 && p.z_out != nullptr) dst = p.z_out + state0 + static_cast<int64_t>(row) * D + slice * kSlice;
+      } else {
+        dst = p.zseg + ((static_cast<int64_t>(unit) * (p.nseg - 1) + seg) * D + row) * kSlice;
+      }
+      if (dst != nullptr) {
+#pragma unroll
+        for (int q = 0; q < kSlice / 4; ++q)
+          reinterpret_cast<float4*>(dst)[q] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+      }
+    }
+  } else if (OUT && warp < 12) {
+    // --------------------------------- masked scores and output, one row per lane
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const float ldf = static_cast<float>(ld);
+    // Row factor against the 32-column block m: forward d^(row - 32m - 31) with the
+    // column power d^(31 - jj); backward d^(32m - row) with d^jj. Both are powers >= 0.
+    float f[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int x = p.reverse ? 32 * m - row : row - 32 * m - 31;
+      f[m] = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_in : p.s_in;
+    }
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const ChunkAt c = chunk_at(p, ci0 + i);
+      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.s_full), i & 1, ctl)))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        uint32_t pk[16];
+        const bool off_diag = p.reverse ? m > quad : m < quad;
+        if (off_diag || m == quad) {
+          uint32_t s[32];
+          tmem_ld32(tS + lane_off + 32 * m, s);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int jj = 2 * j + k;
+              float w;
+              bool keep = true;
+              if (off_diag) {
+                w = f[m] * sm.pow32[p.reverse ? jj : 31 - jj];
+              } else {
+                const int x = p.reverse ? jj - lane : lane - jj;
+                keep = x >= 0;
+                w = p.s_in * sm.pow32[keep ? x : 0];
+              }
+              if (p.reverse) keep = keep && 32 * m + jj < c.len;
+              v[k] = keep ? __uint_as_float(s[jj]) * w : 0.f;
+            }
+            pk[j] = pack_bf16x2(v[0], v[1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
+        }
+        tmem_st16(tS + lane_off + 16 * m, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(smem_addr(&sm.p_ready));
+      const int x = p.reverse ? c.len - 1 - row : row + 1;
+      const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
+      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.y_full), i & 1, ctl)))) break;
+      tc_fence_after();
+      uint32_t out[32];
+#pragma unroll
+      for (int q = 0; q < kSlice; q += 16) {
+        uint32_t az[16], pc[16];
+        tmem_ld16(tAZ + lane_off + q, az);
+        tmem_ld16(tPC + lane_off + q, pc);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          out[q / 2 + k] = pack_bf16x2(fmaf(__uint_as_float(az[2 * k]), w, __uint_as_float(pc[2 * k])),
+                                       fmaf(__uint_as_float(az[2 * k + 1]), w, __uint_as_float(pc[2 * k + 1])));
+      }
+      tc_fence_before();
+      mbar_arrive(smem_addr(&sm.y_free));
+      if (row < c.len) {
+        const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
+        uint4* dst = reinterpret_cast<uint4*>(p.y + (tok * p.H + h) * D + slice * kSlice);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ recurrent form
+// A few tokens on a kept state, updated in place: per (batch, head) the D x D fp32
+// state is read and written once (8 D^2 bytes, the bound) while the tokens' q, k, v are
+// walked from shared memory. A CTA owns CW columns of one head's state: a thread holds
+// rows rg, rg + RG, ... of four columns in registers; each token's output is summed
+// over a warp's row groups by shuffles and over the warps through shared memory.
+template <int D, int CW>
+__global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p) {
+  constexpr int CG = CW / 4;        // column groups of 4
+  constexpr int RG = 256 / CG;      // row groups
+  constexpr int RPT = D / RG;       // rows per thread
+  static_assert(RPT >= 1 && CG <= 32, "tile");
+  __shared__ float sq[kLinStepMaxT][D], sk[kLinStepMaxT][D], sv[kLinStepMaxT][CW];
+  __shared__ float red[2][8][CW];
+  constexpr int kSl = D / CW;
+  const int sl = static_cast<int>(blockIdx.x) % kSl;
+  const int64_t bh = blockIdx.x / kSl;
+  const int h = static_cast<int>(bh % p.H);
+  const int64_t b = bh / p.H;
+  const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* st = p.state + bh * D * D + sl * CW + cg * 4;
+  float4 s[RPT];
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) s[r] = *reinterpret_cast<const float4*>(st + static_cast<int64_t>(rg + r * RG) * D);
+  for (int i = threadIdx.x; i < p.T * D; i += 256) {
+    const int t = i / D, d = i % D;
+    const int64_t at = ((b * p.T + t) * p.H + h) * D + d;
+    sq[t][d] = __bfloat162float(p.q[at]) * p.scale;
+    sk[t][d] = __bfloat162float(p.k[at]);
+    if (d < CW) sv[t][d] = __bfloat162float(p.v[at + sl * CW]);
+  }
+  const float dec = expf(__ldg(p.log_decay + h));
+  __syncthreads();
+  for (int t = 0; t < p.T; ++t) {
+    const float4 v = *reinterpret_cast<const float4*>(&sv[t][cg * 4]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const float kk = sk[t][rg + r * RG], qq = sq[t][rg + r * RG];
+      s[r].x = fmaf(s[r].x, dec, kk * v.x);
+      s[r].y = fmaf(s[r].y, dec, kk * v.y);
+      s[r].z = fmaf(s[r].z, dec, kk * v.z);
+      s[r].w = fmaf(s[r].w, dec, kk * v.w);
+      o.x = fmaf(qq, s[r].x, o.x);
+      o.y = fmaf(qq, s[r].y, o.y);
+      o.z = fmaf(qq, s[r].z, o.z);
+      o.w = fmaf(qq, s[r].w, o.w);
+    }
+#pragma unroll
+    for (int m = CG; m < 32; m <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+    }
+    if (lane < CG) *reinterpret_cast<float4*>(&red[t & 1][warp][lane * 4]) = o;
+    __syncthreads();   // two buffers: the sums of token t are read before those of t + 2 are written
+    if (threadIdx.x < CW) {
+      float y = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) y += red[t & 1][w][threadIdx.x];
+      p.o[((b * p.T + t) * p.H + h) * D + sl * CW + threadIdx.x] = __float2bfloat16_rn(y);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) *reinterpret_cast<float4*>(st + static_cast<int64_t>(rg + r * RG) * D) = s[r];
+}
+
+template <int D, bool OUT>
+cudaError_t launch_lin(const LinLaunch& L, int grid, cudaStream_t stream) {
+  const size_t smem = sizeof(LinSmem<D, OUT>) + 1024;
+  auto kern = linattn_kernel<D, OUT>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kern<<<grid, LinCfg<D, OUT>::kThreads, smem, stream>>>(L.tm_a, L.tm_b, L.tm_c, L.p);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------ host side
+
+// The memory view a plan's tensors are walked in: pieces of consecutive tokens in
+// natural order. A contiguous batch of one, and a single rank, are one piece.
+struct LinView {
+  int N, zigzag, T, piece_len, pieces, chunks_per_piece, nch;
+};
+LinView lin_view(const PlanView& v) {
+  LinView w;
+  const bool plain = v.N == 1 || (v.layout == CP_LAYOUT_CONTIGUOUS && v.B == 1);
+  w.N = plain ? 1 : v.N;
+  w.zigzag = !plain && v.layout == CP_LAYOUT_ZIGZAG;
+  w.T = v.S / w.N;
+  w.pieces = w.zigzag ? 2 * w.N : w.N;
+  w.piece_len = v.S / w.pieces;
+  w.chunks_per_piece = (w.piece_len + kChunk - 1) / kChunk;
+  w.nch = w.pieces * w.chunks_per_piece;
+  return w;
+}
+
+// Segments a sequence is cut into. Modelled time, in chunks of the output launch:
+// waves x chunks per segment, the state launch at half a chunk each, and a fixed cost
+// per launch and wave (pipeline fill). More than kMaxSegments joins too many states.
+constexpr int kMaxSegments = 64;
+int choose_segments(int units, int nch, int sms) {
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= nch && s <= kMaxSegments; ++s) {
+    const double per = (nch + s - 1) / s;
+    const double waves = (static_cast<int64_t>(units) * s + sms - 1) / sms;
+    double cost = waves * (per + 4.0);
+    if (s > 1) {
+      const double w1 = (static_cast<int64_t>(units) * (s - 1) + sms - 1) / sms;
+      cost += w1 * (0.5 * per + 4.0) + 0.1 * s;
+    }
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+size_t scan_workspace(const PlanView& v) {
+  const LinView w = lin_view(v);
+  const int units = v.B * v.H * (v.D / kSlice);
+  const int nseg = choose_segments(units, w.nch, v.sms);
+  return static_cast<size_t>(units) * (nseg - 1) * v.D * kSlice * sizeof(float);
+}
+
+struct ScanCall {
+  const void *a, *b, *c;
+  void* y;
+  const float* z0;
+  bool z0_transposed, reverse;
+  float s_in, s_st, s_upd;
+  float* z_out;
+};
+
+int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float* ws, cudaStream_t stream) {
+  const LinView w = lin_view(v);
+  LinLaunch L;
+  const int64_t rb = static_cast<int64_t>(w.N) * v.B;
+  if (!encode_map_4d(&L.tm_a, s.a, v.D, v.H, w.T, rb, 1, kChunk) ||
+      !encode_map_4d(&L.tm_b, s.b, v.D, v.H, w.T, rb, 1, kChunk) ||
+      !encode_map_4d(&L.tm_c, s.c, v.D, v.H, w.T, rb, 1, kChunk))
+    return CP_ERR_CUDA;
+  LinParams& p = L.p;
+  p.B = v.B;
+  p.H = v.H;
+  p.S = v.S;
+  p.N = w.N;
+  p.T = w.T;
+  p.zigzag = w.zigzag;
+  p.piece_len = w.piece_len;
+  p.chunks_per_piece = w.chunks_per_piece;
+  p.nch = w.nch;
+  p.units = v.B * v.H * (v.D / kSlice);
+  p.nseg = choose_segments(p.units, w.nch, v.sms);
+  p.reverse = s.reverse;
+  p.z0_transposed = s.z0_transposed;
+  p.s_in = s.s_in;
+  p.s_st = s.s_st;
+  p.s_upd = s.s_upd;
+  p.log_decay = log_decay;
+  p.z0 = s.z0;
+  p.z_out = s.z_out;
+  p.zseg = ws;
+  p.y = static_cast<__nv_bfloat16*>(s.y);
+  p.status = v.status;
+  p.wait_limit_ns = kWaitLimitNs;
+  if (p.nseg > 1) {
+    const int grid = p.units * (p.nseg - 1);
+    if ((v.D == 128 ? launch_lin<128, false>(L, grid, stream) : launch_lin<64, false>(L, grid, stream)) != cudaSuccess)
+      return CP_ERR_CUDA;
+  }
+  const int grid = p.units * p.nseg;
+  return (v.D == 128 ? launch_lin<128, true>(L, grid, stream) : launch_lin<64, true>(L, grid, stream)) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+// Arguments common to the forward and the backward.
+int check_plan(cp_attn_plan_t plan, PlanView* v) {
+  const int rc = plan_view(plan, v);
+  if (rc != CP_OK) return rc;
+  if (v->layout == CP_LAYOUT_ULYSSES || !v->causal) return CP_ERR_UNSUPPORTED;
+  // one CTA per 64 columns, (batch, head) and segment, indexed in int32
+  if (static_cast<int64_t>(v->B) * v->H * (v->D / kSlice) > (int64_t(1) << 30) / kMaxSegments) return CP_ERR_UNSUPPORTED;
+  return CP_OK;
+}
+
+}  // namespace
+
+}  // namespace cpattn
+
+using namespace cpattn;
+
+extern "C" {
+
+size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan) {
+  PlanView v;
+  if (plan == nullptr || check_plan(plan, &v) != CP_OK) return 0;
+  return scan_workspace(v);
+}
+
+int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
+                   const float* state_in, void* o, float* state_out, void* workspace, cp_stream_t stream) {
+  if (plan == nullptr || q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || o == nullptr)
+    return CP_ERR_INVALID_ARG;
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(o) || !is_aligned16(state_in) ||
+      !is_aligned16(state_out) || !is_aligned16(workspace) || (reinterpret_cast<uintptr_t>(log_decay) & 3u) != 0)
+    return CP_ERR_ALIGNMENT;
+  if (state_in != nullptr && state_in == state_out) return CP_ERR_INVALID_ARG;   // read by every segment's CTAs
+  PlanView pv;
+  int rc = check_plan(plan, &pv);
+  if (rc != CP_OK) return rc;
+  if (workspace == nullptr && scan_workspace(pv) > 0) return CP_ERR_WORKSPACE;
+  const ScanCall s = {q, k, v, o, state_in, false, false, pv.scale, pv.scale, 1.f, state_out};
+  return run_scan(pv, s, log_decay, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
+                   const void* dout, const float* state_in, const float* dstate_out, void* dq, void* dk, void* dv,
+                   float* dstate_in, void* workspace, cp_stream_t stream) {
+  if (plan == nullptr || q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || dout == nullptr ||
+      dq == nullptr || dk == nullptr || dv == nullptr)
+    return CP_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, dout, state_in, dstate_out, dq, dk, dv, dstate_in, workspace};
+  for (const void* x : ptrs)
+    if (!is_aligned16(x)) return CP_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(log_decay) & 3u) != 0) return CP_ERR_ALIGNMENT;
+  if (dstate_out != nullptr && dstate_out == dstate_in) return CP_ERR_INVALID_ARG;
+  PlanView pv;
+  int rc = check_plan(plan, &pv);
+  if (rc != CP_OK) return rc;
+  if (workspace == nullptr && scan_workspace(pv) > 0) return CP_ERR_WORKSPACE;
+  float* ws = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const float sc = pv.scale;
+  const ScanCall calls[3] = {{dout, v, k, dq, state_in, true, false, sc, sc, 1.f, nullptr},
+                             {v, dout, q, dk, dstate_out, true, true, sc, 1.f, sc, nullptr},
+                             {k, q, dout, dv, dstate_out, false, true, sc, 1.f, sc, dstate_in}};
+  for (const ScanCall& s : calls)   // one after the other on the stream: they share the workspace
+    if ((rc = run_scan(pv, s, log_decay, ws, st)) != CP_OK) return rc;
+  return CP_OK;
+}
+
+int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, float* state, void* o, cp_stream_t stream) {
+  if (B < 0 || T < 0 || H < 1) return CP_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return CP_ERR_UNSUPPORTED;
+  if (T > kLinStepMaxT || static_cast<int64_t>(B) * H * (D / 32) > INT32_MAX) return CP_ERR_UNSUPPORTED;
+  if (!(scale > -INFINITY && scale < INFINITY)) return CP_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return CP_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || state == nullptr || o == nullptr)
+    return CP_ERR_INVALID_ARG;
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(state) || !is_aligned16(o) ||
+      (reinterpret_cast<uintptr_t>(log_decay) & 3u) != 0)
+    return CP_ERR_ALIGNMENT;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return CP_ERR_CUDA;
+  LinStepParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.log_decay = log_decay;
+  p.state = state;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.scale = scale;
+  p.T = T;
+  p.H = H;
+  const int64_t heads = static_cast<int64_t>(B) * H;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Whole heads per CTA when they fill the GPU; else 32 columns each, for more CTAs.
+  const bool wide = heads >= 2 * sms;
+  const int grid = static_cast<int>(heads * (wide ? 1 : D / 32));
+  if (D == 128) {
+    if (wide) linattn_step_kernel<128, 128><<<grid, 256, 0, st>>>(p);
+    else linattn_step_kernel<128, 32><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (wide) linattn_step_kernel<64, 64><<<grid, 256, 0, st>>>(p);
+    else linattn_step_kernel<64, 32><<<grid, 256, 0, st>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // extern "C"

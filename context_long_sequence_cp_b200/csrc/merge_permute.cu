@@ -130,6 +130,11 @@ struct UnitMap {
     const int rho = static_cast<int>(rb / B);
     return (static_cast<int64_t>(g) * B + b) * S + static_cast<int64_t>(rho) * Sl + sl;
   }
+  // Natural flat token b * S + pos of output unit o, whose source is src(o).
+  __device__ __forceinline__ int64_t natural_token(int64_t o, int64_t src_unit) const {
+    if (kind == 0) return dir == 0 ? src_unit : o;
+    return (dir == 0 ? o : src_unit) % (static_cast<int64_t>(B) * S);   // group runs (g*B + b)*S + s
+  }
 };
 
 // One warp per unit; each lane moves 16-byte vectors with a 512-byte stride.
@@ -198,6 +203,110 @@ __global__ void __launch_bounds__(256) rope_permute_kernel(UnitMap m, int64_t un
         w[k] = sm100::pack_bf16x2(xe * c[k] - xo * sn[k], xe * sn[k] + xo * c[k]);
       }
       dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Rotary embedding with one position per axis (time, height, width, ...), fused
+// into the layout map, and its gradient (the inverse rotation fused into the
+// inverse map). Feature pair i of every head of a token is rotated by
+// pos[axis(i)] * theta_i; theta and the axis of each pair are precomputed on the
+// host. Pairs are adjacent features (2i, 2i+1) or the halves (i, i + D/2).
+//
+// Bound: HBM, 2 B read + 2 B written per element. LPU lanes share a unit (a token
+// row, or a Ulysses run of H/N heads); each takes PPL of the D/2 angles (reduced
+// to [-pi, pi] in fp64: positions are full int32), and the lanes exchange the
+// cosines and sines they need by shuffles, so an angle is computed once per unit
+// and not once per head group. A lane always meets the same pairs: the stride
+// LPU is a multiple of the lanes that span a head.
+template <int D, int LPU, bool HALF>
+__global__ void __launch_bounds__(256) rope_axes_kernel(UnitMap m, int64_t units, int vec_per_unit,
+                                                        const __grid_constant__ RopeAxesArgs ra,
+                                                        const int* __restrict__ positions,
+                                                        const uint4* __restrict__ in, uint4* __restrict__ out) {
+  constexpr int kPpl = D / 2 / LPU;          // angles computed per lane
+  constexpr int kNeed = HALF ? 8 : 4;        // pairs a lane rotates
+  constexpr int kLph = D / (2 * kNeed);      // lanes that span a head
+  static_assert(LPU % kLph == 0 && kPpl >= 1 && kPpl <= kNeed, "lanes per unit");
+  constexpr int kU = HALF ? 4 : 8;           // items in flight per lane
+  const int lane = threadIdx.x & 31;
+  const int sub = lane & (LPU - 1);
+  const int c = sub % kLph;
+  const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  constexpr int kGpw = 32 / LPU;             // units per warp
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
+  for (int64_t base = warp0 * kGpw; base < units; base += nwarps * kGpw) {
+    const bool live = base + lane / LPU < units;
+    const int64_t u = live ? base + lane / LPU : units - 1;
+    const int64_t s = m.src(u);
+    // Natural flat token (b * S + position) of the unit.
+    const int64_t tok = m.natural_token(u, s);
+    float cs[kPpl], sn[kPpl];
+#pragma unroll
+    for (int j = 0; j < kPpl; ++j) {
+      const int pair = sub * kPpl + j;
+      const int p = __ldg(positions + ra.axis[pair] * ra.axis_stride + tok);
+      const double a = static_cast<double>(p) * ra.theta[pair];
+      sincosf(static_cast<float>(a - rint(a * kInvTwoPi) * kTwoPi), &sn[j], &cs[j]);
+      if (ra.inverse) sn[j] = -sn[j];
+    }
+    float wc[kNeed], ws[kNeed];
+#pragma unroll
+    for (int k = 0; k < kNeed; ++k) {
+      if constexpr (kPpl == kNeed && LPU == kLph) {
+        wc[k] = cs[k];
+        ws[k] = sn[k];
+      } else {
+        const int owner = (kNeed * c + k) / kPpl;
+        wc[k] = __shfl_sync(0xffffffffu, cs[k % kPpl], owner, LPU);
+        ws[k] = __shfl_sync(0xffffffffu, sn[k % kPpl], owner, LPU);
+      }
+    }
+    const uint4* src = in + s * vec_per_unit;
+    uint4* dst = out + u * vec_per_unit;
+    const int items = live ? (HALF ? vec_per_unit / 2 : vec_per_unit) : 0;
+    for (int i0 = sub; i0 < items; i0 += LPU * kU) {
+      uint4 x[kU], y[HALF ? kU : 1];
+#pragma unroll
+      for (int q = 0; q < kU; ++q) {
+        const int i = i0 + q * LPU;
+        if (i >= items) break;
+        if constexpr (HALF) {
+          const uint4* r = src + (i / kLph) * (D / 8) + c;
+          x[q] = __ldg(r);
+          y[q] = __ldg(r + D / 16);
+        } else {
+          x[q] = __ldg(src + i);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kU; ++q) {
+        const int i = i0 + q * LPU;
+        if (i >= items) break;
+        uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+        if constexpr (HALF) {
+          uint32_t z[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a0 = __uint_as_float(w[k] << 16), a1 = __uint_as_float(w[k] & 0xffff0000u);
+            const float b0 = __uint_as_float(z[k] << 16), b1 = __uint_as_float(z[k] & 0xffff0000u);
+            w[k] = sm100::pack_bf16x2(a0 * wc[2 * k] - b0 * ws[2 * k], a1 * wc[2 * k + 1] - b1 * ws[2 * k + 1]);
+            z[k] = sm100::pack_bf16x2(a0 * ws[2 * k] + b0 * wc[2 * k], a1 * ws[2 * k + 1] + b1 * wc[2 * k + 1]);
+          }
+          uint4* r = dst + (i / kLph) * (D / 8) + c;
+          r[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          r[D / 16] = make_uint4(z[0], z[1], z[2], z[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xffff0000u);
+            w[k] = sm100::pack_bf16x2(a * wc[k] - b * ws[k], a * ws[k] + b * wc[k]);
+          }
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
     }
   }
 }
@@ -276,6 +385,51 @@ cudaError_t launch_rope_permute(const PermuteArgs& a, const RopeArgs& ra, const 
   rope_permute_kernel<<<static_cast<int>(blocks), 256, 0, stream>>>(
       make_map(a), units, vpu, ra, static_cast<const uint4*>(in), static_cast<uint4*>(out));
   return cudaGetLastError();
+}
+
+namespace {
+
+template <int D, int LPU, bool HALF>
+cudaError_t launch_rope_axes_impl(const PermuteArgs& a, const RopeAxesArgs& ra, const int* positions, const void* in,
+                                  void* out, int64_t units, int vpu, cudaStream_t stream) {
+  constexpr int kUnitsPerBlock = 8 * (32 / LPU);
+  int64_t blocks = (units + kUnitsPerBlock - 1) / kUnitsPerBlock;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
+  if (blocks > cap) blocks = cap;
+  rope_axes_kernel<D, LPU, HALF><<<static_cast<int>(blocks), 256, 0, stream>>>(
+      make_map(a), units, vpu, ra, positions, static_cast<const uint4*>(in), static_cast<uint4*>(out));
+  return cudaGetLastError();
+}
+
+// Lanes per unit: the widest power of two (a multiple of the lanes that span a
+// head, at most a warp) that the unit's heads fill.
+template <int D, bool HALF>
+cudaError_t launch_rope_axes_d(const PermuteArgs& a, const RopeAxesArgs& ra, const int* positions, const void* in,
+                               void* out, int64_t units, int heads, cudaStream_t stream) {
+  constexpr int kLph = HALF ? D / 16 : D / 8;
+  const int vpu = heads * (D / 8);
+  if (heads * kLph >= 32) return launch_rope_axes_impl<D, 32, HALF>(a, ra, positions, in, out, units, vpu, stream);
+  if constexpr (kLph <= 16)
+    if (heads * kLph >= 16) return launch_rope_axes_impl<D, 16, HALF>(a, ra, positions, in, out, units, vpu, stream);
+  if constexpr (kLph <= 8)
+    if (heads * kLph >= 8) return launch_rope_axes_impl<D, 8, HALF>(a, ra, positions, in, out, units, vpu, stream);
+  if constexpr (kLph <= 4)
+    return launch_rope_axes_impl<D, 4, HALF>(a, ra, positions, in, out, units, vpu, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_axes(const PermuteArgs& a, const RopeAxesArgs& ra, const int* positions, const void* in,
+                             void* out, cudaStream_t stream) {
+  const int64_t units = a.kind == 0 ? static_cast<int64_t>(a.B) * a.S : static_cast<int64_t>(a.N) * a.B * a.S;
+  if (units == 0) return cudaSuccess;
+  const int heads = a.kind == 0 ? a.H : a.H / a.N;
+  if (a.D == 128)
+    return ra.half ? launch_rope_axes_d<128, true>(a, ra, positions, in, out, units, heads, stream)
+                   : launch_rope_axes_d<128, false>(a, ra, positions, in, out, units, heads, stream);
+  return ra.half ? launch_rope_axes_d<64, true>(a, ra, positions, in, out, units, heads, stream)
+                 : launch_rope_axes_d<64, false>(a, ra, positions, in, out, units, heads, stream);
 }
 
 cudaError_t launch_index_map(const PermuteArgs& a, int64_t* map_out, cudaStream_t stream) {

@@ -415,6 +415,94 @@ CP_API int cp_layout_permute(cp_attn_plan_t plan, int direction, const void* in,
 CP_API int cp_rope_permute(cp_attn_plan_t plan, const void* in, void* out, double base, int64_t pos_offset,
                            cp_stream_t stream);
 
+/*
+ * Rotary position embedding with one position per axis (time, height, width of a
+ * video or image token, or any explicit position, such as the shared depth of
+ * drafted tokens), fused into the layout map; and its gradient. Same page and
+ * section as cp_rope_permute: positions are global, so they are given per natural
+ * token and do not depend on the layout. The D/2 feature pairs are cut into `axes`
+ * runs of sections[a] pairs; pair i of axis a turns by positions[a][b][s] * theta_i:
+ *   CP_ROPE_FREQS_SHARED    theta_i = base^(-2i/D), one table over all pairs
+ *   CP_ROPE_FREQS_PER_AXIS  theta = base^(-j/n), j the pair's index within the n
+ *                           pairs of its axis
+ *   CP_ROPE_PAIRS_ADJACENT  pair i = features (2i, 2i+1), as cp_rope_permute
+ *   CP_ROPE_PAIRS_HALF      pair i = features (i, i + D/2)
+ * direction 0: `in` natural [B][S][H][D] (Ulysses: shards), `out` the attention input
+ *   layout, as cp_rope_permute. direction 1, the gradient: `in` in the attention input
+ *   layout, `out` natural (shards), turned by the negative angle.
+ *   positions : int32 [axes][B][S], device, any values, natural token order
+ *   sections  : int [axes], host, each >= 1, their sum D/2 (CP_ERR_INVALID_ARG)
+ * base > 1. Angles are reduced to [-pi, pi] in fp64, rotated in fp32, rounded to bf16
+ * once. `in` and `out` must not overlap; both 16-byte, positions 4-byte aligned
+ * (CP_ERR_ALIGNMENT). The plan's device must be current (CP_ERR_INVALID_ARG).
+ */
+enum { CP_ROPE_FREQS_SHARED = 0, CP_ROPE_FREQS_PER_AXIS = 1 };
+enum { CP_ROPE_PAIRS_ADJACENT = 0, CP_ROPE_PAIRS_HALF = 1 };
+CP_API int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* in, void* out,
+                                const int32_t* positions, int axes, const int* sections, double base, int freqs,
+                                int pairing, cp_stream_t stream);
+
+/*
+ * Causal linear attention with a decay for each head, on the tensors of a causal
+ * contiguous or zigzag plan (CP_ERR_UNSUPPORTED otherwise): the layers without a
+ * softmax that long-context models mix with softmax attention, in the same layout, so
+ * that no permutation stands between the two kinds. No page prints it; it is, per
+ * (batch, head), over natural positions t:
+ *   S_t = d S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   d = exp(log_decay[h]),
+ * scale the plan's. d lies in [0, 1]: log_decay <= 0, -inf allowed. The state joins
+ * context-parallel ranks that hold consecutive tokens: each runs on its own tokens
+ * from its predecessor's last state.
+ *   q, k, v   : bf16, the plan's layout, device
+ *   log_decay : float32 [H], device, 4-byte aligned
+ *   state_in  : float32 [B][H][D][D] (row = feature of k, column = feature of v), the
+ *               state before token 0, device; NULL for zero
+ *   o         : bf16, q's layout, device (written)
+ *   state_out : float32 [B][H][D][D], the state after the last token, device (written);
+ *               may be NULL; must not overlap state_in
+ *   workspace : device, cp_linattn_workspace_bytes(plan) bytes (NULL if 0)
+ * The state is held and summed in fp32; the decayed scores and the state that the
+ * queries read are rounded to bf16 once, as tensor-core operands. Values must be
+ * finite: within a chunk of 128 tokens a NaN or infinity also reaches the tokens before
+ * it. One or two kernels; nothing is allocated; results do not depend on timing. Waits
+ * that run out are reported by cp_attn_check. The plan's device must be current
+ * (CP_ERR_INVALID_ARG).
+ */
+CP_API int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
+                          const float* state_in, void* o, float* state_out, void* workspace, cp_stream_t stream);
+
+/*
+ * Gradients of cp_linattn_fwd (log_decay is a constant of the layer and has none):
+ *   dq_i = scale (sum_{j<=i} d^(i-j) (do_i . v_j) k_j + d^(i+1) S_in do_i)
+ *   dk_j = scale sum_{i>=j} d^(i-j) (do_i . v_j) q_i + d^(S-1-j) G v_j
+ *   dv_j = scale sum_{i>=j} d^(i-j) (q_i . k_j) do_i + d^(S-1-j) G^T k_j
+ *   dstate_in = scale sum_i d^(i+1) q_i do_i^T + d^S G,   G = dstate_out.
+ *   dout       : bf16, q's layout, device
+ *   state_in   : the forward's, or NULL
+ *   dstate_out : float32 [B][H][D][D], the gradient of state_out, or NULL for zero
+ *   dq, dk, dv : bf16, q's layout, device (written)
+ *   dstate_in  : float32 [B][H][D][D], device (written); may be NULL; must not overlap
+ *                dstate_out
+ *   workspace  : device, cp_linattn_workspace_bytes(plan) bytes (NULL if 0)
+ */
+CP_API int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
+                          const void* dout, const float* state_in, const float* dstate_out, void* dq, void* dk,
+                          void* dv, float* dstate_in, void* workspace, cp_stream_t stream);
+
+/* Workspace bytes of cp_linattn_fwd and cp_linattn_bwd on this plan (0 where none is
+ * needed, and for a plan they do not support). */
+CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
+
+/*
+ * The recurrent form of the same operator: T <= 16 new tokens of each sequence (one
+ * when decoding) on a state kept between calls, in fp32 throughout.
+ *   q, k, v : bf16 [B][T][H][D], device;   o : bf16 [B][T][H][D], device (written)
+ *   state   : float32 [B][H][D][D], device, read and updated in place
+ * D 64 or 128 (CP_ERR_UNSUPPORTED otherwise, and for T > 16); B = 0 or T = 0 does
+ * nothing. Enqueued on `stream` of the current device.
+ */
+CP_API int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, const void* v,
+                           const float* log_decay, float scale, float* state, void* o, cp_stream_t stream);
+
 /* Length of the index map written by cp_layout_index_map: B*S for
  * contiguous/zigzag (one entry per token), N*B*S for Ulysses (one entry per
  * (group, batch, token) run of H/N heads). */
