@@ -19,17 +19,17 @@
 // Four products on the tensor core per chunk; the chunk's decay mask is built from 32
 // powers of d and three row factors, so no exponential is taken per score.
 //
-// A CTA owns 64 columns of C (and of Z) of one (batch, head) and walks a run of
-// chunks ("segment"); Z stays in the registers of one warpgroup in fp32. Sequences with
-// few (batch, head) are cut into segments: a first launch (OUT = false) computes each
-// segment's own state, and the second joins those before it at its start.
+// A CTA walks a run of chunks ("segment") of one (batch, head); Z stays in the registers
+// of eight warps in fp32. Sequences with few (batch, head) are cut into segments: a first
+// launch (OUT = false) computes each segment's own state, and the second joins those
+// before it at its start.
 //
 // Precision. The state is exact to fp32: the weighted rows of C are split into three
-// bf16 terms (8 + 8 + 8 bits of the fp32 product) that are multiplied side by side as
-// one N = 192 operand and summed smallest first; the chunk sum starts from zero in TMEM
-// and is added to d^L Z in registers, d^L as an fp32 pair, because the tensor core's
-// accumulation truncates and a long run of it would drift. Rounded to bf16: the masked
-// scores (P), and the state where it is multiplied by A (Z); both once, as operands.
+// bf16 terms (8 + 8 + 8 bits of the fp32 product) multiplied one after the other; the
+// chunk sum starts from zero in TMEM and is added to d^L Z in registers, d^L as an fp32
+// pair, because the tensor core's accumulation truncates and a long run of it would
+// drift. Rounded to bf16: the masked scores (P), and the state where it is multiplied
+// by A (Z); both once, as operands.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,41 +48,64 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kChunk = 128;     // tokens of a chunk: the 128 lanes of a tcgen05 product
-constexpr int kSlice = 64;      // columns of C and Z per CTA
+constexpr int kChunk = 128;          // tokens of a chunk: the 128 lanes of a tcgen05 product
 constexpr int kBlk = kChunk * 128;   // 128 rows x 128 B: one swizzled 64-column block
+constexpr int kPart = 32;            // rows of C weighted and multiplied at a time
+constexpr int kParts = kChunk / kPart;
+constexpr int kPartBlk = kPart * 128;
 
 template <int D, bool OUT>
 struct LinCfg {
-  static constexpr int kWide = kChunk * D * 2;            // a 128 x D tile
-  static constexpr int kStageBytes = (OUT ? 2 : 1) * kWide + kBlk;
-  static constexpr int kStages = OUT ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 4);
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kTileBytes = kBlocks * kBlk;       // a 128 x D tile
+  static constexpr int kPerChunk = OUT ? 3 : 2;           // tiles per chunk: B, [A,] C
+  static constexpr int kTiles = D == 128 ? (OUT ? 4 : 5) : (OUT ? 9 : 8);
   static constexpr int kThreads = OUT ? 448 : 320;
   static constexpr int kMmaWarp = OUT ? 12 : 8;
-  // TMEM columns: chunk state [0,192), and with OUT the scores/P [192,320),
-  // A Z [320,384), P C [384,448).
-  static constexpr int kTmemCols = OUT ? 512 : 256;
+  static constexpr int kTerm = kBlocks * kPartBlk;        // one term of a part of weighted C
+  // TMEM columns: chunk state [0,128), and with OUT the scores/P [128,256),
+  // A Z [256,384), P C [384,512).
+  static constexpr int kTmemCols = OUT ? 512 : 128;
 };
-constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);    // A B^T
-constexpr uint32_t kIdescKV = idesc_bf16_f32(128, 192, 1, 1);   // B^T C (both MN-major)
-constexpr uint32_t kIdescY = idesc_bf16_f32(128, 64, 0, 1);     // A Z, P C
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // A B^T
+__host__ __device__ constexpr uint32_t idesc_kv(int D) { return idesc_bf16_f32(128, D, 1, 1); }   // B^T C (both MN-major)
+__host__ __device__ constexpr uint32_t idesc_y(int D) { return idesc_bf16_f32(128, D, 0, 1); }    // A Z, P C
 
 template <int D, bool OUT>
 struct alignas(1024) LinSmem {
-  // Stage: [A tile] B tile, C slice. For D = 64 the state product's upper 64 rows
-  // (unused) read the block after B, which is the C slice.
-  uint8_t stage[LinCfg<D, OUT>::kStages][LinCfg<D, OUT>::kStageBytes];
-  uint8_t cs[3][kBlk];                    // weighted C: high, middle, low terms
-  uint8_t z[OUT ? D * 128 : 16];          // bf16 state, row = feature of A
-  uint64_t full[LinCfg<D, OUT>::kStages], empty[LinCfg<D, OUT>::kStages];
-  uint64_t s_full, p_ready, cs_ready, kv_done, zq_done, z_ready, y_full, y_free, drain;
-  float pow32[32];                        // d^0 .. d^31
+  // Ring of 128 x D tiles. For D = 64 the state product's upper 64 rows (unused)
+  // read the 16 KB after a tile, which stay inside this struct.
+  uint8_t tile[LinCfg<D, OUT>::kTiles][LinCfg<D, OUT>::kTileBytes];
+  uint8_t cs[2][3 * LinCfg<D, OUT>::kTerm];   // weighted C: low, middle, high terms
+  uint8_t z[OUT ? D * D * 2 : 1024];          // bf16 state, row = feature of A
+  uint64_t full[LinCfg<D, OUT>::kTiles], empty[LinCfg<D, OUT>::kTiles];
+  uint64_t cs_ready[2], cs_free[2];
+  uint64_t s_full, p_ready, kv_done, kv_free, qz_done, z_ready, y_full, y_free, drain;
+  alignas(16) float pow32[64];                // [32 + x] = d^x for x = 0 .. 31, 0 below
   uint32_t tmem_base;
   WaitBlock wblk;
 };
 static_assert(sizeof(LinSmem<128, true>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
 static_assert(sizeof(LinSmem<64, true>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
 static_assert(sizeof(LinSmem<128, false>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, false>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, false>::cs) + sizeof(LinSmem<64, false>::z) >= kBlk, "over-read of the last tile");
+static_assert(sizeof(LinSmem<64, true>::cs) + sizeof(LinSmem<64, true>::z) >= kBlk, "over-read of the last tile");
+
+// Descriptor moved by a byte offset (the address field counts 16-byte units).
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// 32 bytes of a row; one 32-byte sector per thread where the address allows it.
+__device__ __forceinline__ void st_row32(void* p, const uint32_t* v, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 
 // d^n; n = 0 gives 1 also for d = 0.
 __device__ __forceinline__ double decay_pow(double ld, int64_t n) {
@@ -94,8 +117,9 @@ struct ChunkAt {
   int rank, t0, len;
   int before;   // tokens walked before it
 };
+template <bool REV>
 __device__ __forceinline__ ChunkAt chunk_at(const LinParams& p, int ci) {
-  const int cn = p.reverse ? p.nch - 1 - ci : ci;
+  const int cn = REV ? p.nch - 1 - ci : ci;
   const int piece = cn / p.chunks_per_piece;
   const int off = (cn - piece * p.chunks_per_piece) * kChunk;
   ChunkAt c;
@@ -108,31 +132,31 @@ __device__ __forceinline__ ChunkAt chunk_at(const LinParams& p, int ci) {
     c.t0 = (piece < p.N ? 0 : p.piece_len) + off;
   }
   const int p0 = piece * p.piece_len + off;
-  c.before = p.reverse ? p.S - p0 - c.len : p0;
+  c.before = REV ? p.S - p0 - c.len : p0;
   return c;
 }
+template <bool REV>
 __device__ __forceinline__ int walked_before(const LinParams& p, int ci) {
-  return ci >= p.nch ? p.S : chunk_at(p, ci).before;
+  return ci >= p.nch ? p.S : chunk_at<REV>(p, ci).before;
 }
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-template <int D, bool OUT>
+template <int D, bool OUT, bool REV>
 __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
     linattn_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ LinParams p) {
   using C = LinCfg<D, OUT>;
-  constexpr int NS = C::kStages;
+  constexpr int NT = C::kTiles;
+  constexpr uint32_t kIdescKV = idesc_kv(D), kIdescY = idesc_y(D);
+  constexpr int kTB = 0, kTA = 1, kTC = OUT ? 2 : 1;   // order of a chunk's tiles in the ring
   extern __shared__ uint8_t smem_raw[];
   LinSmem<D, OUT>& sm = *reinterpret_cast<LinSmem<D, OUT>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  constexpr int kSlices = D / kSlice;
-  const int unit = static_cast<int>(blockIdx.x) % p.units;
+  const int bh = static_cast<int>(blockIdx.x) % p.units;
   const int seg = static_cast<int>(blockIdx.x) / p.units;
-  const int slice = unit % kSlices;
-  const int bh = unit / kSlices;
   const int h = bh % p.H, b = bh / p.H;
   const int ci0 = static_cast<int>(static_cast<int64_t>(seg) * p.nch / p.nseg);
   const int ci1 = static_cast<int>(static_cast<int64_t>(seg + 1) * p.nch / p.nseg);
@@ -140,23 +164,28 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
   const double ld = static_cast<double>(__ldg(p.log_decay + h));
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < NT; ++s) {
       mbar_init(smem_addr(&sm.full[s]), 1);
       mbar_init(smem_addr(&sm.empty[s]), 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&sm.cs_ready[s]), 256);
+      mbar_init(smem_addr(&sm.cs_free[s]), 1);
+    }
     mbar_init(smem_addr(&sm.s_full), 1);
     mbar_init(smem_addr(&sm.p_ready), 128);
-    mbar_init(smem_addr(&sm.cs_ready), 128);
     mbar_init(smem_addr(&sm.kv_done), 1);
-    mbar_init(smem_addr(&sm.zq_done), 1);
-    mbar_init(smem_addr(&sm.z_ready), 128);
+    mbar_init(smem_addr(&sm.kv_free), 256);
+    mbar_init(smem_addr(&sm.qz_done), 1);
+    mbar_init(smem_addr(&sm.z_ready), 256);
     mbar_init(smem_addr(&sm.y_full), 1);
     mbar_init(smem_addr(&sm.y_free), 128);
     mbar_init(smem_addr(&sm.drain), 1);
     wait_block_init(sm.wblk, p.status, p.wait_limit_ns);
     fence_barrier_init();
   }
-  if (threadIdx.x < 32) sm.pow32[threadIdx.x] = static_cast<float>(decay_pow(ld, threadIdx.x));
+  if (threadIdx.x < 64)
+    sm.pow32[threadIdx.x] = threadIdx.x < 32 ? 0.f : static_cast<float>(decay_pow(ld, threadIdx.x - 32));
   if (warp == C::kMmaWarp) {
     tmem_alloc(smem_addr(&sm.tmem_base), C::kTmemCols);
     tmem_relinquish();
@@ -171,155 +200,135 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl ctl = wait_ctl(sm.wblk);
-  constexpr uint32_t kOffB = OUT ? C::kWide : 0, kOffC = kOffB + C::kWide;
-  const uint32_t tS = tbase + 192, tAZ = tbase + 320, tPC = tbase + 384;
+  const uint32_t tS = tbase + 128, tAZ = tbase + 256, tPC = tbase + 384;
+  auto tile_full = [&](int t) { return all_ok(mbar_wait(smem_addr(&sm.full[t % NT]), (t / NT) & 1, ctl)); };
 
   if (warp == C::kMmaWarp + 1) {
     // ---------------------------------------------------------------- TMA
     const uint64_t pol = l2_policy_evict_first();
     bool ok = true;
-    int i = 0;
-    for (; i < n; ++i) {
-      const int st = i % NS;
-      if (i >= NS) ok = all_ok(mbar_wait(smem_addr(&sm.empty[st]), (i / NS - 1) & 1, ctl));
-      if (!ok) break;
-      const ChunkAt c = chunk_at(p, ci0 + i);
-      const uint32_t bar = smem_addr(&sm.full[st]);
-      const uint32_t dst = smem_addr(&sm.stage[st][0]);
+    int t = 0;
+    for (int i = 0; i < n && ok; ++i) {
+      const ChunkAt c = chunk_at<REV>(p, ci0 + i);
       const int rb = c.rank * p.B + b;
-      mbar_arrive_expect_tx_elect(bar, C::kStageBytes);
-      for (int blk = 0; blk < kSlices; ++blk)
-        tma_load_4d_elect(dst + kOffB + blk * kBlk, &tm_b, bar, blk * 64, h, c.t0, rb, pol);
-      tma_load_4d_elect(dst + kOffC, &tm_c, bar, slice * 64, h, c.t0, rb, pol);
-      if constexpr (OUT)
-        for (int blk = 0; blk < kSlices; ++blk)
-          tma_load_4d_elect(dst + blk * kBlk, &tm_a, bar, blk * 64, h, c.t0, rb, pol);
+      for (int which = 0; which < C::kPerChunk; ++which, ++t) {
+        const int st = t % NT;
+        if (t >= NT) ok = all_ok(mbar_wait(smem_addr(&sm.empty[st]), (t / NT - 1) & 1, ctl));
+        if (!ok) break;
+        const uint32_t bar = smem_addr(&sm.full[st]);
+        const CUtensorMap* map = which == kTB ? &tm_b : which == kTC ? &tm_c : &tm_a;
+        mbar_arrive_expect_tx_elect(bar, C::kTileBytes);
+        for (int blk = 0; blk < C::kBlocks; ++blk)
+          tma_load_4d_elect(smem_addr(&sm.tile[st][0]) + blk * kBlk, map, bar, blk * 64, h, c.t0, rb, pol);
+      }
     }
     if (!ok)   // abort: let every load this warp issued land before the CTA exits
-      for (int k = i - NS; k < i; ++k)
-        if (k >= 0) mbar_wait_drain(smem_addr(&sm.full[k % NS]), (k / NS) & 1, p.wait_limit_ns);
+      for (int k = t - NT; k < t; ++k)
+        if (k >= 0) mbar_wait_drain(smem_addr(&sm.full[k % NT]), (k / NT) & 1, p.wait_limit_ns);
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA
+    const uint64_t d_z = smem_desc_sw128(smem_addr(&sm.z[0]), D * 128, 1024);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int st = i % NS;
-      const uint32_t base = smem_addr(&sm.stage[st][0]);
-      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.full[st]), (i / NS) & 1, ctl)))) break;
-      tc_fence_after();
+      const int tB = i * C::kPerChunk + kTB, tA = i * C::kPerChunk + kTA, tC = i * C::kPerChunk + kTC;
+      const uint32_t aB = smem_addr(&sm.tile[tB % NT][0]), aA = smem_addr(&sm.tile[tA % NT][0]),
+                     aC = smem_addr(&sm.tile[tC % NT][0]);
+      if (!(ok = tile_full(tB))) break;
       if constexpr (OUT) {
+        if (!(ok = tile_full(tA))) break;
+        tc_fence_after();
         // Scores. P of the previous chunk shares the columns: its product was issued before.
+        const uint64_t dA = smem_desc_sw128(aA, 16, 1024), dB = smem_desc_sw128(aB, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
-          umma_ss_elect(tS, smem_desc_sw128(base + off, 16, 1024), smem_desc_sw128(base + kOffB + off, 16, 1024),
-                        kIdescS, kk > 0);
+          umma_ss_elect(tS, desc_at(dA, off), desc_at(dB, off), kIdescS, kk > 0);
         }
         umma_commit_elect(smem_addr(&sm.s_full));
-      }
-      // Chunk state: its TMEM columns are free once the state warpgroup has read the
-      // previous chunk's (with OUT it then also published the state before this chunk).
-      if (OUT || i > 0)
-        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.z_ready), (OUT ? i : i - 1) & 1, ctl)))) break;
-      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.cs_ready), i & 1, ctl)))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < kChunk / 16; ++kk)
-        umma_ss_elect(tbase, smem_desc_sw128(base + kOffB + kk * 2048, kBlk, 1024),
-                      smem_desc_sw128(smem_addr(&sm.cs[0][0]) + kk * 2048, kBlk, 1024), kIdescKV, kk > 0);
-      umma_commit_elect(smem_addr(&sm.kv_done));
-      if constexpr (OUT) {
-        if (i > 0)
-          if (!(ok = all_ok(mbar_wait(smem_addr(&sm.y_free), (i - 1) & 1, ctl)))) break;
+        // A Z, onto the columns the output warps have read for the previous chunk.
+        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.z_ready), i & 1, ctl)))) break;
+        if (i > 0 && !(ok = all_ok(mbar_wait(smem_addr(&sm.y_free), (i - 1) & 1, ctl)))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_elect(tAZ, smem_desc_sw128(base + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024),
-                        smem_desc_sw128(smem_addr(&sm.z[0]) + kk * 2048, kBlk, 1024), kIdescY, kk > 0);
-        umma_commit_elect(smem_addr(&sm.zq_done));
+          umma_ss_elect(tAZ, desc_at(dA, (kk >> 2) * kBlk + (kk & 3) * 32), desc_at(d_z, kk * 2048), kIdescY,
+                        kk > 0);
+        umma_commit_elect(smem_addr(&sm.qz_done));
+        umma_commit_elect(smem_addr(&sm.empty[tA % NT]));
+      }
+      // Chunk state, part by part as the weighted rows of C come, smallest term first.
+      if (i > 0 && !(ok = all_ok(mbar_wait(smem_addr(&sm.kv_free), (i - 1) & 1, ctl)))) break;
+      const uint64_t dBt = smem_desc_sw128(aB, kBlk, 1024);
+      for (int part = 0; part < kParts; ++part) {
+        const int buf = part & 1, use = (i * kParts + part) >> 1;
+        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.cs_ready[buf]), use & 1, ctl)))) break;
+        tc_fence_after();
+        const uint64_t dCs = smem_desc_sw128(smem_addr(&sm.cs[buf][0]), kPartBlk, 1024);
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int kk = 0; kk < kPart / 16; ++kk)
+            umma_ss_elect(tbase, desc_at(dBt, part * kPartBlk + kk * 2048), desc_at(dCs, term * C::kTerm + kk * 2048),
+                          kIdescKV, part > 0 || term > 0 || kk > 0);
+        umma_commit_elect(smem_addr(&sm.cs_free[buf]));
+      }
+      if (!ok) break;
+      umma_commit_elect(smem_addr(&sm.kv_done));
+      umma_commit_elect(smem_addr(&sm.empty[tB % NT]));
+      if constexpr (OUT) {
+        if (!(ok = tile_full(tC))) break;
         if (!(ok = all_ok(mbar_wait(smem_addr(&sm.p_ready), i & 1, ctl)))) break;
         tc_fence_after();
+        const uint64_t dC = smem_desc_sw128(aC, kBlk, 1024);
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
-          umma_ts_elect(tPC, tS + kk * 8, smem_desc_sw128(base + kOffC + kk * 2048, kBlk, 1024), kIdescY, kk > 0);
+          umma_ts_elect(tPC, tS + kk * 8, desc_at(dC, kk * 2048), kIdescY, kk > 0);
         umma_commit_elect(smem_addr(&sm.y_full));
       }
-      umma_commit_elect(smem_addr(&sm.empty[st]));
+      umma_commit_elect(smem_addr(&sm.empty[tC % NT]));
     }
     if (n > 0) {   // every product and commit has to finish before TMEM is freed
       umma_commit_elect(smem_addr(&sm.drain));
       mbar_wait_drain(smem_addr(&sm.drain), 0, p.wait_limit_ns);
     }
-  } else if (warp < 4) {
-    // ------------------------------------------- weighted C, in three bf16 terms
-    const int row = threadIdx.x;
-    float w_full = 0.f;
-    {
-      const int x = p.reverse ? row + 1 : kChunk - 1 - row;
-      w_full = static_cast<float>(decay_pow(ld, x)) * p.s_upd;
-    }
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int st = i % NS;
-      const ChunkAt c = chunk_at(p, ci0 + i);
-      float w = w_full;
-      if (!p.reverse && c.len < kChunk && row < c.len)
-        w = static_cast<float>(decay_pow(ld, c.len - 1 - row)) * p.s_upd;
-      const bool live = row < c.len;
-      ok = all_ok(mbar_wait(smem_addr(&sm.full[st]), (i / NS) & 1, ctl));
-      if (ok && i > 0) ok = all_ok(mbar_wait(smem_addr(&sm.kv_done), (i - 1) & 1, ctl));
-      if (!ok) break;
-      const uint8_t* src = &sm.stage[st][kOffC] + row * 128;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int at = (j ^ (row & 7)) * 16;   // 128-byte swizzle of the 16-byte vector
-        const uint4 v = *reinterpret_cast<const uint4*>(src + at);
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t t0[4], t1[4], t2[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float x0 = live ? __uint_as_float(in[q] << 16) * w : 0.f;
-          const float x1 = live ? __uint_as_float(in[q] & 0xffff0000u) * w : 0.f;
-          t0[q] = pack_bf16x2(x0, x1);
-          const float r0 = x0 - __uint_as_float(t0[q] << 16), r1 = x1 - __uint_as_float(t0[q] & 0xffff0000u);
-          t1[q] = pack_bf16x2(r0, r1);
-          t2[q] = pack_bf16x2(r0 - __uint_as_float(t1[q] << 16), r1 - __uint_as_float(t1[q] & 0xffff0000u));
-        }
-        const int dst = row * 128 + at;
-        *reinterpret_cast<uint4*>(&sm.cs[0][dst]) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-        *reinterpret_cast<uint4*>(&sm.cs[1][dst]) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4*>(&sm.cs[2][dst]) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(smem_addr(&sm.cs_ready));
-    }
   } else if (warp < 8) {
-    // --------------------------------------------------------- state, one row per lane
+    // ------------------------------------ weighted C in three bf16 terms, and the state
+    const int crow = threadIdx.x >> 3, cvec = threadIdx.x & 7;   // row of a part, 16-byte vector of a block
     const int quad = warp & 3;
-    const int row = quad * 32 + lane;        // feature of B (row of Z)
+    const int row = quad * 32 + lane;          // feature of B (row of Z)
+    const int col0 = (warp >> 2) * (D / 2);    // columns of Z held by this thread
     const bool live = row < D;
-    const uint32_t tKV = tbase + (static_cast<uint32_t>(quad * 32) << 16);
-    float z[kSlice];
+    const uint32_t tKV = tbase + (static_cast<uint32_t>(quad * 32) << 16) + col0;
+    const int tail = p.piece_len % kChunk;
+    float w_full[kParts], w_tail[kParts];      // weights of this thread's rows of C, 0 past a tail chunk's tokens
 #pragma unroll
-    for (int q = 0; q < kSlice; ++q) z[q] = 0.f;
+    for (int part = 0; part < kParts; ++part) {
+      const int r = part * kPart + crow;
+      w_full[part] = static_cast<float>(decay_pow(ld, REV ? r + 1 : kChunk - 1 - r)) * p.s_upd;
+      w_tail[part] = r < tail ? static_cast<float>(decay_pow(ld, REV ? r + 1 : tail - 1 - r)) * p.s_upd : 0.f;
+    }
+    const double d_full = decay_pow(ld, kChunk), d_tail = decay_pow(ld, tail);
+    float z[D / 2];
+#pragma unroll
+    for (int q = 0; q < D / 2; ++q) z[q] = 0.f;
     const int64_t state0 = static_cast<int64_t>(bh) * D * D;
     if (OUT && live) {
-      const int x = walked_before(p, ci0);
+      const int x = walked_before<REV>(p, ci0);
       if (p.z0 != nullptr) {
         const float w = static_cast<float>(decay_pow(ld, x));
 #pragma unroll
-        for (int q = 0; q < kSlice; ++q) {
-          const int col = slice * kSlice + q;
-          const int64_t at = p.z0_transposed ? static_cast<int64_t>(col) * D + row : static_cast<int64_t>(row) * D + col;
-          z[q] = w * __ldg(p.z0 + state0 + at);
+        for (int q = 0; q < D / 2; ++q) {
+          const int col = col0 + q;
+          z[q] = w * __ldg(p.z0 + state0 + (p.z0_transposed ? col * D + row : row * D + col));
         }
       }
       for (int g = 0; g < seg; ++g) {
-        const int end = walked_before(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
+        const int end = walked_before<REV>(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
         const float w = static_cast<float>(decay_pow(ld, x - end));
         const float4* src = reinterpret_cast<const float4*>(
-            p.zseg + ((static_cast<int64_t>(unit) * (p.nseg - 1) + g) * D + row) * kSlice);
+            p.zseg + ((static_cast<int64_t>(bh) * (p.nseg - 1) + g) * D + row) * D + col0);
 #pragma unroll
-        for (int q = 0; q < kSlice / 4; ++q) {
+        for (int q = 0; q < D / 8; ++q) {
           const float4 v = src[q];
           z[4 * q] = fmaf(w, v.x, z[4 * q]);
           z[4 * q + 1] = fmaf(w, v.y, z[4 * q + 1]);
@@ -328,58 +337,92 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
         }
       }
     }
-    auto publish = [&]() {   // bf16 state for A Z
+    auto publish = [&]() {   // bf16 state for A Z: 64-column blocks of D rows x 128 B
       if (live) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(&sm.z[row * 128 + ((j ^ (row & 7)) * 16)]) =
-              make_uint4(pack_bf16x2(z[8 * j], z[8 * j + 1]), pack_bf16x2(z[8 * j + 2], z[8 * j + 3]),
-                         pack_bf16x2(z[8 * j + 4], z[8 * j + 5]), pack_bf16x2(z[8 * j + 6], z[8 * j + 7]));
+        for (int v = 0; v < D / 16; ++v) {
+          const int col = col0 + 8 * v;
+          *reinterpret_cast<uint4*>(&sm.z[(col / 64) * (D * 128) + row * 128 + ((((col % 64) / 8) ^ (row & 7)) * 16)]) =
+              make_uint4(pack_bf16x2(z[8 * v], z[8 * v + 1]), pack_bf16x2(z[8 * v + 2], z[8 * v + 3]),
+                         pack_bf16x2(z[8 * v + 4], z[8 * v + 5]), pack_bf16x2(z[8 * v + 6], z[8 * v + 7]));
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    };
-    if constexpr (OUT) {
-      publish();
       mbar_arrive(smem_addr(&sm.z_ready));
-    }
-    const double dfull = decay_pow(ld, kChunk);
-    const int tail = p.piece_len % kChunk;
-    const double dtail = decay_pow(ld, tail);
+    };
+    if constexpr (OUT) publish();
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const ChunkAt c = chunk_at(p, ci0 + i);
-      const double dl = c.len == kChunk ? dfull : dtail;
-      const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
-      if (!(ok = all_ok(mbar_wait(smem_addr(OUT ? &sm.zq_done : &sm.kv_done), i & 1, ctl)))) break;
+      const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
+      const int tC = i * C::kPerChunk + kTC;
+      if (!(ok = tile_full(tC))) break;
+      const uint8_t* src = &sm.tile[tC % NT][0];
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const int buf = part & 1, use = (i * kParts + part) >> 1;
+        if (use > 0 && !(ok = all_ok(mbar_wait(smem_addr(&sm.cs_free[buf]), (use - 1) & 1, ctl)))) break;
+        const float w = whole ? w_full[part] : w_tail[part];
+        const bool keep = whole || part * kPart + crow < tail;   // other rows may follow in memory
+        const int swz = crow * 128 + ((cvec ^ (crow & 7)) * 16);
+#pragma unroll
+        for (int blk = 0; blk < C::kBlocks; ++blk) {
+          uint4 v = *reinterpret_cast<const uint4*>(src + blk * kBlk + part * kPartBlk + swz);
+          if (!keep) v = make_uint4(0, 0, 0, 0);
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t t0[4], t1[4], t2[4];
+          const uint64_t ww = f2_pack(w, w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float x0, x1;
+            const uint64_t x = f2_mul(bf16x2_to_f2(in[q]), ww);
+            f2_unpack(x, x0, x1);
+            t0[q] = pack_bf16x2(x0, x1);
+            const uint64_t r = f2_sub(x, bf16x2_to_f2(t0[q]));
+            f2_unpack(r, x0, x1);
+            t1[q] = pack_bf16x2(x0, x1);
+            f2_unpack(f2_sub(r, bf16x2_to_f2(t1[q])), x0, x1);
+            t2[q] = pack_bf16x2(x0, x1);
+          }
+          uint8_t* dst = &sm.cs[buf][blk * kPartBlk + swz];
+          *reinterpret_cast<uint4*>(dst) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+          *reinterpret_cast<uint4*>(dst + C::kTerm) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(dst + 2 * C::kTerm) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(smem_addr(&sm.cs_ready[buf]));
+      }
+      if (!ok) break;
+      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.kv_done), i & 1, ctl)))) break;
       tc_fence_after();
+      const double dl = whole ? d_full : d_tail;
+      const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
       if (quad * 32 < D) {
 #pragma unroll
-        for (int q = 0; q < kSlice; q += 16) {
-          uint32_t t0[16], t1[16], t2[16];
-          tmem_ld16(tKV + q, t0);
-          tmem_ld16(tKV + 64 + q, t1);
-          tmem_ld16(tKV + 128 + q, t2);
+        for (int q = 0; q < D / 2; q += 32) {
+          uint32_t t0[32];
+          tmem_ld32(tKV + q, t0);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float sum = __uint_as_float(t0[k]) + (__uint_as_float(t1[k]) + __uint_as_float(t2[k]));
-            z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, sum));
-          }
+          for (int k = 0; k < 32; ++k) z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, __uint_as_float(t0[k])));
         }
       }
       tc_fence_before();
-      if (OUT && i + 1 < n) publish();
-      if (i + 1 < n) mbar_arrive(smem_addr(&sm.z_ready));
+      if (i + 1 < n) {
+        mbar_arrive(smem_addr(&sm.kv_free));
+        if constexpr (OUT) {
+          if (!(ok = all_ok(mbar_wait(smem_addr(&sm.qz_done), i & 1, ctl)))) break;
+          publish();
+        }
+      }
     }
     if (ok && live) {
       float* dst = nullptr;
-      if (OUT) {
-        if (seg == p.nseg - 1 && p.z_out != nullptr) dst = p.z_out + state0 + static_cast<int64_t>(row) * D + slice * kSlice;
-      } else {
-        dst = p.zseg + ((static_cast<int64_t>(unit) * (p.nseg - 1) + seg) * D + row) * kSlice;
-      }
+      if (!OUT)
+        dst = p.zseg + ((static_cast<int64_t>(bh) * (p.nseg - 1) + seg) * D + row) * D + col0;
+      else if (seg == p.nseg - 1 && p.z_out != nullptr)
+        dst = p.z_out + state0 + row * D + col0;
       if (dst != nullptr) {
 #pragma unroll
-        for (int q = 0; q < kSlice / 4; ++q)
+        for (int q = 0; q < D / 8; ++q)
           reinterpret_cast<float4*>(dst)[q] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
       }
     }
@@ -389,77 +432,84 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const float ldf = static_cast<float>(ld);
-    // Row factor against the 32-column block m: forward d^(row - 32m - 31) with the
-    // column power d^(31 - jj); backward d^(32m - row) with d^jj. Both are powers >= 0.
+    const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31u) == 0;
+    // Decay of score (row, 32m + jj), exponent |row - column| >= 0: off the diagonal block
+    // (m != quad) a row factor times a column power, forward d^(row - 32m - 31) d^(31 - jj),
+    // backward d^(32m - row) d^jj; on it d^|lane - jj| from the table.
     float f[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int x = p.reverse ? 32 * m - row : row - 32 * m - 31;
+      const int x = REV ? 32 * m - row : row - 32 * m - 31;
       f[m] = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_in : p.s_in;
     }
+    const float4* off = reinterpret_cast<const float4*>(&sm.pow32[32]);
+    const float* diag = &sm.pow32[32 + (REV ? -lane : lane)];   // column jj at REV ? +jj : -jj
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const ChunkAt c = chunk_at(p, ci0 + i);
+      const ChunkAt c = chunk_at<REV>(p, ci0 + i);
       if (!(ok = all_ok(mbar_wait(smem_addr(&sm.s_full), i & 1, ctl)))) break;
       tc_fence_after();
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         uint32_t pk[16];
-        const bool off_diag = p.reverse ? m > quad : m < quad;
-        if (off_diag || m == quad) {
-          uint32_t s[32];
-          tmem_ld32(tS + lane_off + 32 * m, s);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int jj = 2 * j + k;
-              float w;
-              bool keep = true;
-              if (off_diag) {
-                w = f[m] * sm.pow32[p.reverse ? jj : 31 - jj];
-              } else {
-                const int x = p.reverse ? jj - lane : lane - jj;
-                keep = x >= 0;
-                w = p.s_in * sm.pow32[keep ? x : 0];
-              }
-              if (p.reverse) keep = keep && 32 * m + jj < c.len;
-              v[k] = keep ? __uint_as_float(s[jj]) * w : 0.f;
-            }
-            pk[j] = pack_bf16x2(v[0], v[1]);
-          }
-        } else {
+        if (REV ? m < quad : m > quad) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) pk[j] = 0u;
+        } else {
+          uint32_t s[32];
+          tmem_ld32(tS + lane_off + 32 * m, s);
+          if (REV && c.len < kChunk) {   // columns past the chunk's tokens hold other rows
+#pragma unroll
+            for (int jj = 0; jj < 32; ++jj) s[jj] = 32 * m + jj < c.len ? s[jj] : 0u;
+          }
+          if (m == quad) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int j0 = 2 * j, j1 = 2 * j + 1;
+              const float w0 = diag[REV ? j0 : -j0] * p.s_in, w1 = diag[REV ? j1 : -j1] * p.s_in;
+              const bool k0 = REV ? j0 >= lane : j0 <= lane, k1 = REV ? j1 >= lane : j1 <= lane;
+              pk[j] = pack_bf16x2(k0 ? __uint_as_float(s[j0]) * w0 : 0.f, k1 ? __uint_as_float(s[j1]) * w1 : 0.f);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 v = off[REV ? q : 7 - q];
+              const float w[4] = {REV ? v.x : v.w, REV ? v.y : v.z, REV ? v.z : v.y, REV ? v.w : v.x};
+              pk[2 * q] = pack_bf16x2(__uint_as_float(s[4 * q]) * (f[m] * w[0]),
+                                      __uint_as_float(s[4 * q + 1]) * (f[m] * w[1]));
+              pk[2 * q + 1] = pack_bf16x2(__uint_as_float(s[4 * q + 2]) * (f[m] * w[2]),
+                                          __uint_as_float(s[4 * q + 3]) * (f[m] * w[3]));
+            }
+          }
         }
         tmem_st16(tS + lane_off + 16 * m, pk);
       }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(smem_addr(&sm.p_ready));
-      const int x = p.reverse ? c.len - 1 - row : row + 1;
+      const int x = REV ? c.len - 1 - row : row + 1;
       const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
+      const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
+      __nv_bfloat16* dst = p.y + (tok * p.H + h) * D;
       if (!(ok = all_ok(mbar_wait(smem_addr(&sm.y_full), i & 1, ctl)))) break;
       tc_fence_after();
-      uint32_t out[32];
 #pragma unroll
-      for (int q = 0; q < kSlice; q += 16) {
-        uint32_t az[16], pc[16];
-        tmem_ld16(tAZ + lane_off + q, az);
-        tmem_ld16(tPC + lane_off + q, pc);
+      for (int q = 0; q < D; q += 32) {
+        uint32_t az[32], pc[32], out[16];
+        tmem_ld32(tAZ + lane_off + q, az);
+        tmem_ld32(tPC + lane_off + q, pc);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          out[q / 2 + k] = pack_bf16x2(fmaf(__uint_as_float(az[2 * k]), w, __uint_as_float(pc[2 * k])),
-                                       fmaf(__uint_as_float(az[2 * k + 1]), w, __uint_as_float(pc[2 * k + 1])));
-      }
-      tc_fence_before();
-      mbar_arrive(smem_addr(&sm.y_free));
-      if (row < c.len) {
-        const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
-        uint4* dst = reinterpret_cast<uint4*>(p.y + (tok * p.H + h) * D + slice * kSlice);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+        for (int k = 0; k < 16; ++k)
+          out[k] = pack_bf16x2(fmaf(__uint_as_float(az[2 * k]), w, __uint_as_float(pc[2 * k])),
+                               fmaf(__uint_as_float(az[2 * k + 1]), w, __uint_as_float(pc[2 * k + 1])));
+        if (q + 32 == D) {
+          tc_fence_before();
+          mbar_arrive(smem_addr(&sm.y_free));
+        }
+        if (row < c.len) {
+          st_row32(dst + q, out, wide);
+          st_row32(dst + q + 16, out + 8, wide);
+        }
       }
     }
   }
@@ -541,15 +591,23 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
   for (int r = 0; r < RPT; ++r) *reinterpret_cast<float4*>(st + static_cast<int64_t>(rg + r * RG) * D) = s[r];
 }
 
-template <int D, bool OUT>
+template <int D, bool OUT, bool REV>
 cudaError_t launch_lin(const LinLaunch& L, int grid, cudaStream_t stream) {
   const size_t smem = sizeof(LinSmem<D, OUT>) + 1024;
-  auto kern = linattn_kernel<D, OUT>;
+  auto kern = linattn_kernel<D, OUT, REV>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   kern<<<grid, LinCfg<D, OUT>::kThreads, smem, stream>>>(L.tm_a, L.tm_b, L.tm_c, L.p);
   return cudaGetLastError();
+}
+
+// The launches of one scan: the segments' own states (all but the last), then the rows.
+template <int D, bool REV>
+bool launch_scan(const LinLaunch& L, cudaStream_t stream) {
+  const LinParams& p = L.p;
+  if (p.nseg > 1 && launch_lin<D, false, REV>(L, p.units * (p.nseg - 1), stream) != cudaSuccess) return false;
+  return launch_lin<D, true, REV>(L, p.units * p.nseg, stream) == cudaSuccess;
 }
 
 // ------------------------------------------------------------------------ host side
@@ -597,9 +655,9 @@ int choose_segments(int units, int nch, int sms) {
 
 size_t scan_workspace(const PlanView& v) {
   const LinView w = lin_view(v);
-  const int units = v.B * v.H * (v.D / kSlice);
+  const int units = v.B * v.H;
   const int nseg = choose_segments(units, w.nch, v.sms);
-  return static_cast<size_t>(units) * (nseg - 1) * v.D * kSlice * sizeof(float);
+  return static_cast<size_t>(units) * (nseg - 1) * v.D * v.D * sizeof(float);
 }
 
 struct ScanCall {
@@ -629,7 +687,7 @@ int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float
   p.piece_len = w.piece_len;
   p.chunks_per_piece = w.chunks_per_piece;
   p.nch = w.nch;
-  p.units = v.B * v.H * (v.D / kSlice);
+  p.units = v.B * v.H;
   p.nseg = choose_segments(p.units, w.nch, v.sms);
   p.reverse = s.reverse;
   p.z0_transposed = s.z0_transposed;
@@ -643,15 +701,9 @@ int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float
   p.y = static_cast<__nv_bfloat16*>(s.y);
   p.status = v.status;
   p.wait_limit_ns = kWaitLimitNs;
-  if (p.nseg > 1) {
-    const int grid = p.units * (p.nseg - 1);
-    if ((v.D == 128 ? launch_lin<128, false>(L, grid, stream) : launch_lin<64, false>(L, grid, stream)) != cudaSuccess)
-      return CP_ERR_CUDA;
-  }
-  const int grid = p.units * p.nseg;
-  return (v.D == 128 ? launch_lin<128, true>(L, grid, stream) : launch_lin<64, true>(L, grid, stream)) == cudaSuccess
-             ? CP_OK
-             : CP_ERR_CUDA;
+  const bool ok = v.D == 128 ? (s.reverse ? launch_scan<128, true>(L, stream) : launch_scan<128, false>(L, stream))
+                             : (s.reverse ? launch_scan<64, true>(L, stream) : launch_scan<64, false>(L, stream));
+  return ok ? CP_OK : CP_ERR_CUDA;
 }
 
 // Arguments common to the forward and the backward.
@@ -659,8 +711,8 @@ int check_plan(cp_attn_plan_t plan, PlanView* v) {
   const int rc = plan_view(plan, v);
   if (rc != CP_OK) return rc;
   if (v->layout == CP_LAYOUT_ULYSSES || !v->causal) return CP_ERR_UNSUPPORTED;
-  // one CTA per 64 columns, (batch, head) and segment, indexed in int32
-  if (static_cast<int64_t>(v->B) * v->H * (v->D / kSlice) > (int64_t(1) << 30) / kMaxSegments) return CP_ERR_UNSUPPORTED;
+  // one CTA per (batch, head) and segment, indexed in int32
+  if (static_cast<int64_t>(v->B) * v->H > (int64_t(1) << 30) / kMaxSegments) return CP_ERR_UNSUPPORTED;
   return CP_OK;
 }
 

@@ -15,7 +15,7 @@ struct LinParams {
   int zigzag;
   int piece_len;            // consecutive tokens in memory and in the sequence
   int chunks_per_piece, nch;
-  int units;                // B * H * (D / 64)
+  int units;                // B * H
   int nseg;                 // segments a sequence is cut into
   int reverse;              // walk from the last token to the first
   int z0_transposed;
@@ -23,7 +23,7 @@ struct LinParams {
   const float* log_decay;   // [H]
   const float* z0;          // [B][H][D][D] or null
   float* z_out;             // [B][H][D][D] or null
-  float* zseg;              // [units][nseg - 1][D][64]: each segment's own state
+  float* zseg;              // [units][nseg - 1][D][D]: each segment's own state
   __nv_bfloat16* y;
   int* status;
   uint64_t wait_limit_ns;
