@@ -47,6 +47,12 @@ SIGNATURES = {
     "cp_linattn_bwd": (_I, [_P] * 14),
     "cp_linattn_workspace_bytes": (_SZ, [_P]),
     "cp_linattn_step": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _F, _P, _P, _P]),
+    "cp_cache_plan": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _I, _F]),
+    "cp_cache_plan_destroy": (_I, [_P]),
+    "cp_cache_attn_workspace_bytes": (_SZ, [_P]),
+    "cp_cache_attn": (_I, [_P] * 10),
+    "cp_cache_attn_partial": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "cp_cache_check": (_I, [_P, _P]),
     "cp_layout_index_map_len": (_I64, [_P]),
     "cp_layout_index_map": (_I, [_P, _P, _P]),
     "cp_attn_check": (_I, [_P, _P]),
@@ -585,6 +591,105 @@ def linattn_step(q, k, v, log_decay, state, scale: float = 0.0, o=None, stream=N
         return y
 
     return _enqueue(dev, stream, body)
+
+
+class CachePlan:
+    """Sizes of an attention over a key/value cache (wraps ``cp_cache_plan``): B sequences,
+    Hq query and Hkv key/value heads, ``capacity`` cache rows, T new tokens per call."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, D: int, capacity: int, T: int = 1, softmax_scale: float = 0.0):
+        self.B, self.Hq, self.Hkv, self.D, self.capacity, self.T = B, Hq, Hkv, D, capacity, T
+        h = ctypes.c_void_p()
+        _check("cp_cache_plan", lib().cp_cache_plan(ctypes.byref(h), B, Hq, Hkv, D, capacity, T, float(softmax_scale)))
+        self._h = h
+        self._ws = int(lib().cp_cache_attn_workspace_bytes(h))
+
+    @property
+    def handle(self):
+        return self._h
+
+    def workspace_bytes(self) -> int:
+        return self._ws
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            lib().cp_cache_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _cache_inputs(plan, q, k_cache, v_cache, lengths, tree, workspace):
+    dev = q.device
+    _expect("q", q, torch.bfloat16, (plan.B, plan.T, plan.Hq, plan.D), dev)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(name, t, torch.bfloat16, (plan.B, plan.capacity, plan.Hkv, plan.D), dev)
+    _expect("lengths", lengths, torch.int32, (plan.B,), dev)
+    if tree is not None:
+        _expect("tree", tree, torch.int64, (plan.B, plan.T), dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous() or
+                                  workspace.numel() * workspace.element_size() < plan.workspace_bytes()):
+        raise ValueError(f"workspace: expected {plan.workspace_bytes()} contiguous bytes on {dev}")
+    return dev
+
+
+def cache_attn(plan: CachePlan, q, k_cache, v_cache, lengths, tree=None, o=None, lse=None, workspace=None,
+               stream=None):
+    """``cp_cache_attn``: T new tokens of each sequence against its cache.
+
+    q: bf16 [B, T, Hq, D]; k_cache, v_cache: bf16 [B, capacity, Hkv, D] with the new
+    tokens' rows at lengths[b] .. lengths[b] + T - 1; lengths: int32 [B]; tree: int64
+    [B, T], bit u of tree[b, t] set where token t sees new token u (None: a chain).
+    Returns (o bf16 [B, T, Hq, D], lse fp32 [B, Hq, T])."""
+    dev = _cache_inputs(plan, q, k_cache, v_cache, lengths, tree, workspace)
+    if o is not None:
+        _expect("o", o, torch.bfloat16, q.shape, dev)
+    if lse is not None:
+        _expect("lse", lse, torch.float32, (plan.B, plan.Hq, plan.T), dev)
+
+    def body(s):
+        y = torch.empty_like(q) if o is None else o
+        z = torch.empty(plan.B, plan.Hq, plan.T, dtype=torch.float32, device=dev) if lse is None else lse
+        ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        _check("cp_cache_attn",
+               lib().cp_cache_attn(plan.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                   lengths.data_ptr(), _opt(tree), y.data_ptr(), z.data_ptr(), ws.data_ptr(), s))
+        return y, z
+
+    return _enqueue(dev, stream, body)
+
+
+def cache_attn_partial(plan: CachePlan, q, k_cache, v_cache, lengths, own_drafts: bool, tree=None, o_part=None,
+                       lse_part=None, workspace=None, stream=None):
+    """``cp_cache_attn_partial``: one rank's share of a divided cache, as (o_part fp32
+    [B*T*Hq, D], lse_part fp32 [B*T*Hq]) for ``merge_partials``."""
+    dev = _cache_inputs(plan, q, k_cache, v_cache, lengths, tree, workspace)
+    rows = plan.B * plan.T * plan.Hq
+    if o_part is not None:
+        _expect("o_part", o_part, torch.float32, (rows, plan.D), dev)
+    if lse_part is not None:
+        _expect("lse_part", lse_part, torch.float32, (rows,), dev)
+
+    def body(s):
+        y = torch.empty(rows, plan.D, dtype=torch.float32, device=dev) if o_part is None else o_part
+        z = torch.empty(rows, dtype=torch.float32, device=dev) if lse_part is None else lse_part
+        ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        _check("cp_cache_attn_partial",
+               lib().cp_cache_attn_partial(plan.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                           lengths.data_ptr(), int(bool(own_drafts)), _opt(tree), y.data_ptr(),
+                                           z.data_ptr(), ws.data_ptr(), s))
+        return y, z
+
+    return _enqueue(dev, stream, body)
+
+
+def cache_check(plan: CachePlan, stream=None) -> int:
+    """``cp_cache_check``: synchronise and return the recorded status (0 = ok)."""
+    return int(lib().cp_cache_check(plan.handle, _stream(stream)))
 
 
 def attn_bwd(plan: Plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, workspace=None, stream=None):

@@ -1,0 +1,678 @@
+// cache_attn.cu — attention of a few new tokens of each sequence over its key/value
+// cache (sm_100a, tcgen05 + TMEM + TMA): single tokens when decoding, chains or trees of
+// drafted tokens when several are checked at once.
+//
+// The rows of a product are the (token, query head) pairs that share a key/value head,
+// so a cache row is read once for all of them. Token t sees the cached keys
+// [0, lengths[b]) and, among the drafted ones (cache rows lengths[b] + u), those whose
+// bit u is set in its tree word. Softmax, lse and partials are those of attn_fwd.cu.
+//
+// Bound: HBM, the cache read once (4 D bytes per key and key/value head). The 128-key
+// tiles of all (sequence, head, query tile) units are laid end to end and cut into equal
+// runs, one per CTA (one CTA per SM), so uneven lengths leave no SM idle. A run that
+// covers a unit whole writes its output; pieces of a unit go to fp32 slots, two per CTA,
+// that a second kernel joins by their maxima. Within a CTA two softmax warpgroups take
+// the even and the odd key tiles, each with its own maximum, sum and accumulator (joined
+// at the unit's end), so that one's softmax runs under the other's products.
+//
+// Cache rows past the last key are never read as values: their scores are set to -inf
+// and their rows of V are cleared in shared memory, so stale NaNs there do no harm.
+#include "cache_attn.h"
+
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "cp_attn.h"
+#include "geometry.h"
+#include "plan_view.h"
+#include "sm100.cuh"
+#include "softmax.cuh"
+
+namespace cpattn {
+
+namespace {
+
+constexpr int kCacheThreads = 384;
+constexpr float kCacheRescale = 8.0f;   // log2 units: rescale when the maximum grows by > 256x
+constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+constexpr int kBlock = kTile * 128;     // 128 rows x 128 B
+
+template <int D>
+struct CacheCfg {
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kTileBytes = kBlocks * kBlock;
+  static constexpr int kStages = D == 128 ? 5 : 11;
+};
+
+template <int D>
+struct alignas(1024) CacheSmem {
+  uint8_t q[CacheCfg<D>::kTileBytes];
+  uint8_t kv[CacheCfg<D>::kStages][CacheCfg<D>::kTileBytes];
+  uint64_t kv_full[CacheCfg<D>::kStages], kv_empty[CacheCfg<D>::kStages];
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_done[2], ml_ready, unit_done, drain;
+  float2 ml[2][kTile];               // (max, sum) of each warpgroup's rows
+  int before[kCacheMaxB + 1];        // key tiles of the sequences before b
+  int warp_sum[kCacheThreads / 32];
+  uint32_t tmem_base;
+  WaitBlock wblk;
+};
+static_assert(sizeof(CacheSmem<128>) + 1024 <= 232448, "CacheSmem exceeds the per-CTA limit");
+static_assert(sizeof(CacheSmem<64>) + 1024 <= 232448, "CacheSmem exceeds the per-CTA limit");
+
+// Keys of sequence b: cached plus drafted; -1 for a length outside the cache.
+__device__ __forceinline__ int key_count(const CacheParams& p, int b) {
+  const int len = __ldg(p.lengths + b), extra = p.own ? p.T : 0;
+  return len < 0 || len > p.cap - extra ? -1 : len + extra;
+}
+
+// Prefix sums of the sequences' key tiles, by all threads of the block.
+template <int THREADS>
+__device__ __forceinline__ void tile_prefix(const CacheParams& p, int* before, int* warp_sum) {
+  int carry = 0;
+  if (threadIdx.x == 0) before[0] = 0;
+  for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int v = b < p.B ? (max(key_count(p, b), 0) + kTile - 1) / kTile : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if ((threadIdx.x & 31) >= o) v += u;
+    }
+    if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int base = carry;
+    for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) base += warp_sum[w];
+    if (b < p.B) before[b + 1] = base + v;
+    for (int w = 0; w < THREADS / 32; ++w) carry += warp_sum[w];
+    __syncthreads();
+  }
+}
+
+// A run of key tiles of one unit (sequence b, key/value head hk, query tile rt).
+struct CacheSeg {
+  int b, hk, rt;
+  int t0, n, nt;   // key tiles [t0, t0 + n) of nt
+};
+// The piece of the flattened tiles that starts at f and ends at `end` at most.
+__device__ __forceinline__ CacheSeg seg_at(const CacheParams& p, const int* before, int64_t f, int64_t end) {
+  const int hr = p.Hkv * p.row_tiles;
+  int lo = 0, hi = p.B - 1;   // last b with before[b] * hr <= f: never an empty sequence
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(before[mid]) * hr <= f) lo = mid;
+    else hi = mid - 1;
+  }
+  CacheSeg s;
+  s.b = lo;
+  s.nt = before[lo + 1] - before[lo];
+  const int64_t rem = f - static_cast<int64_t>(before[lo]) * hr;
+  const int u = static_cast<int>(rem / s.nt);
+  s.t0 = static_cast<int>(rem - static_cast<int64_t>(u) * s.nt);
+  s.hk = u / p.row_tiles;
+  s.rt = u - s.hk * p.row_tiles;
+  const int64_t left = end - f;
+  s.n = static_cast<int>(left < s.nt - s.t0 ? left : s.nt - s.t0);
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tS, uint32_t q, uint32_t k) {
+  const uint64_t dq = smem_desc_sw128(q, 16, 1024), dk = smem_desc_sw128(k, 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
+    umma_ss_elect(tS, dq + off, dk + off, kIdescQK, kk > 0);
+  }
+}
+template <int D, int KK0, int KK1>
+__device__ __forceinline__ void issue_av(uint32_t tO, uint32_t tP, uint32_t v, bool accumulate) {
+  const uint64_t dv = smem_desc_sw128(v, kBlock, 1024);
+#pragma unroll
+  for (int kk = KK0; kk < KK1; ++kk)
+    umma_ts_elect(tO, tP + kk * 8, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), accumulate || kk > 0);
+}
+
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t shifted(uint64_t w, int s) {
+  return s >= 64 || s <= -64 ? 0ull : s >= 0 ? w << s : w >> -s;
+}
+
+// Row r of the query tile: which token and query head, and where its results go.
+struct CacheRow {
+  bool valid;
+  int t, hq;
+};
+__device__ __forceinline__ CacheRow cache_row(const CacheParams& p, int hk, int rt, int r) {
+  CacheRow c;
+  const int tl = r / p.G;
+  c.t = rt * p.tok_per_tile + tl;
+  c.hq = hk * p.G + (r - tl * p.G);
+  c.valid = tl < p.tok_per_tile && c.t < p.T;
+  return c;
+}
+__device__ __forceinline__ void store_lse(const CacheParams& p, int b, const CacheRow& c, float lse) {
+  if (p.lse == nullptr) return;
+  if (p.o_part != nullptr) p.lse[(static_cast<int64_t>(b) * p.T + c.t) * p.Hq + c.hq] = lse;
+  else p.lse[(static_cast<int64_t>(b) * p.Hq + c.hq) * p.T + c.t] = lse;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kCacheThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheParams p) {
+  using C = CacheCfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  CacheSmem<D>& sm = *reinterpret_cast<CacheSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                      ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_addr(&sm.kv_full[s]), 1);
+      mbar_init(smem_addr(&sm.kv_empty[s]), 1);
+    }
+    mbar_init(smem_addr(&sm.q_full), 1);
+    mbar_init(smem_addr(&sm.q_empty), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_addr(&sm.s_full[w]), 1);
+      mbar_init(smem_addr(&sm.p_full[w][0]), 128);
+      mbar_init(smem_addr(&sm.p_full[w][1]), 128);
+      mbar_init(smem_addr(&sm.o_done[w]), 1);
+    }
+    mbar_init(smem_addr(&sm.ml_ready), 256);
+    mbar_init(smem_addr(&sm.unit_done), 256);
+    mbar_init(smem_addr(&sm.drain), 1);
+    wait_block_init(sm.wblk, p.status, p.wait_limit_ns);
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  tile_prefix<kCacheThreads>(p, sm.before, sm.warp_sum);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const WaitCtl ctl = wait_ctl(sm.wblk);
+  const int64_t total = static_cast<int64_t>(sm.before[p.B]) * p.Hkv * p.row_tiles;
+  const int64_t f0 = total * blockIdx.x / p.n_cta, f1 = total * (blockIdx.x + 1) / p.n_cta;
+  auto wait = [&](uint64_t& bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(smem_addr(&bar), phase & 1, ctl)); };
+
+  if (warp == 9) {
+    // ---------------------------------------------------------------- TMA
+    const uint64_t pol = l2_policy_evict_first();
+    bool ok = true;
+    int kv = 0, unit = 0;
+    for (int64_t f = f0; f < f1 && ok; ++unit) {
+      const CacheSeg s = seg_at(p, sm.before, f, f1);
+      f += s.n;
+      if (unit > 0 && !(ok = wait(sm.q_empty, unit - 1))) break;
+      mbar_arrive_expect_tx_elect(smem_addr(&sm.q_full), C::kBlocks * p.G * p.tok_per_tile * 128);
+      for (int blk = 0; blk < C::kBlocks; ++blk)
+        tma_load_4d_elect(smem_addr(&sm.q[0]) + blk * kBlock, &tm_q, smem_addr(&sm.q_full), blk * 64, s.hk * p.G,
+                          s.rt * p.tok_per_tile, s.b, pol);
+      // K(0), K(1), then V(i), K(i + 2): the order the products take them.
+      for (int j = 0; j < 2 * s.n; ++j, ++kv) {
+        const int key = j == 0 ? 0 : s.n == 1 ? -1 : j == 1 ? 1 : (j & 1) && (j + 1) / 2 < s.n ? (j + 1) / 2 : -1;
+        const int tile = key >= 0 ? key : j == 2 * s.n - 1 ? s.n - 1 : (j - 2) / 2;
+        const int st = kv % NS;
+        if (kv >= NS && !(ok = wait(sm.kv_empty[st], kv / NS - 1))) break;
+        mbar_arrive_expect_tx_elect(smem_addr(&sm.kv_full[st]), C::kTileBytes);
+        for (int blk = 0; blk < C::kBlocks; ++blk)
+          tma_load_4d_elect(smem_addr(&sm.kv[st][0]) + blk * kBlock, key >= 0 ? &tm_k : &tm_v,
+                            smem_addr(&sm.kv_full[st]), blk * 64, s.hk, (s.t0 + tile) * kTile, s.b, pol);
+      }
+    }
+    if (!ok) {   // abort: let every load this warp issued land before the CTA exits
+      for (int k = kv - NS; k < kv; ++k)
+        if (k >= 0) mbar_wait_drain(smem_addr(&sm.kv_full[k % NS]), (k / NS) & 1, p.wait_limit_ns);
+      if (unit > 0) mbar_wait_drain(smem_addr(&sm.q_full), (unit - 1) & 1, p.wait_limit_ns);
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA
+    const uint32_t q = smem_addr(&sm.q[0]);
+    const uint32_t tS[2] = {tbase, tbase + 128}, tO[2] = {tbase + 256, tbase + 256 + D};
+    bool ok = true, issued = false;
+    int kv = 0, unit = 0, cnt[2] = {0, 0};
+    for (int64_t f = f0; f < f1 && ok; ++unit) {
+      const CacheSeg s = seg_at(p, sm.before, f, f1);
+      f += s.n;
+      if (!(ok = wait(sm.q_full, unit))) break;
+      for (int i = 0; i < 2 && i < s.n; ++i, ++kv) {
+        const int st = kv % NS;
+        if (!(ok = wait(sm.kv_full[st], kv / NS))) break;
+        tc_fence_after();
+        issue_qk<D>(tS[i], q, smem_addr(&sm.kv[st][0]));
+        umma_commit_elect(smem_addr(&sm.s_full[i]));
+        umma_commit_elect(smem_addr(&sm.kv_empty[st]));
+        issued = true;
+      }
+      for (int i = 0; i < s.n && ok; ++i) {
+        const int w = i & 1;
+        const int vs = kv % NS;
+        if (!(ok = wait(sm.kv_full[vs], kv / NS))) break;
+        ++kv;
+        const bool next = i + 2 < s.n;
+        int ks = 0;
+        if (next) {
+          ks = kv % NS;
+          if (!(ok = wait(sm.kv_full[ks], kv / NS))) break;
+          ++kv;
+        }
+        const uint32_t v = smem_addr(&sm.kv[vs][0]);
+        if (!(ok = wait(sm.p_full[w][0], cnt[w]))) break;
+        tc_fence_after();
+        issue_av<D, 0, 4>(tO[w], tS[w] + 64, v, i >= 2);
+        if (!(ok = wait(sm.p_full[w][1], cnt[w]))) break;
+        tc_fence_after();
+        issue_av<D, 4, 8>(tO[w], tS[w] + 64, v, true);
+        ++cnt[w];
+        if (i + 2 >= s.n) umma_commit_elect(smem_addr(&sm.o_done[w]));
+        umma_commit_elect(smem_addr(&sm.kv_empty[vs]));
+        if (next) {
+          issue_qk<D>(tS[w], q, smem_addr(&sm.kv[ks][0]));
+          umma_commit_elect(smem_addr(&sm.s_full[w]));
+          umma_commit_elect(smem_addr(&sm.kv_empty[ks]));
+        }
+      }
+      if (!ok) break;
+      umma_commit_elect(smem_addr(&sm.q_empty));
+    }
+    if (issued) {   // every product and commit has to finish before TMEM is freed
+      umma_commit_elect(smem_addr(&sm.drain));
+      mbar_wait_drain(smem_addr(&sm.drain), 0, p.wait_limit_ns);
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int wg = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + lane_off + wg * 128;
+    const uint32_t tO = tbase + lane_off + 256 + wg * D;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int kv = 0, unit = 0, s_cnt = 0, od_cnt = 0;
+    for (int64_t f = f0; f < f1 && ok; ++unit) {
+      const CacheSeg sg = seg_at(p, sm.before, f, f1);
+      f += sg.n;
+      const CacheRow cr = cache_row(p, sg.hk, sg.rt, row);
+      const bool busy = __any_sync(0xffffffffu, cr.valid);   // a warp without rows only keeps the barriers' pace
+      const int len = __ldg(p.lengths + sg.b), keys = len + (p.own ? p.T : 0);
+      uint64_t word = 0;   // drafted tokens this row sees
+      if (p.own && cr.valid)
+        word = p.tree == nullptr ? low_bits(cr.t + 1)
+                                 : __ldg(p.tree + static_cast<int64_t>(sg.b) * p.T + cr.t) & low_bits(p.T);
+      // The accumulators and (max, sum) rows of the unit before have been read by both warpgroups.
+      if (unit > 0 && !(ok = wait(sm.unit_done, unit - 1))) break;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int i = wg; i < sg.n; i += 2) {
+        if (!(ok = wait(sm.s_full[wg], s_cnt))) break;
+        ++s_cnt;
+        tc_fence_after();
+        const int k0 = (sg.t0 + i) * kTile;
+        if (keys - k0 < kTile) {
+          // The unit's last tile: clear the rows of V past its last key (its load is the
+          // last of the run), whatever the cache holds there.
+          const int idx = kv + 2 * sg.n - 1;
+          if (!(ok = wait(sm.kv_full[idx % NS], idx / NS))) break;
+          uint8_t* v = &sm.kv[idx % NS][0];
+          for (int e = row; e < (kTile - (keys - k0)) * 8 * C::kBlocks; e += 128) {
+            const int vec = e % (8 * C::kBlocks), r = keys - k0 + e / (8 * C::kBlocks);
+            *reinterpret_cast<uint4*>(v + (vec / 8) * kBlock + r * 128 + (vec % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (busy) {
+          float s[kTile];
+          tmem_ld128(tS, reinterpret_cast<uint32_t*>(s));
+          const bool masked = k0 + kTile > len;
+          const int lim = len - k0;
+          const uint64_t keep0 = low_bits(lim) | shifted(word, lim), keep1 = low_bits(lim - 64) | shifted(word, lim - 64);
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) s[j] = ((j < 64 ? keep0 : keep1) >> (j & 63)) & 1 ? s[j] : -INFINITY;
+          }
+          // Online softmax with a lazily moved maximum, as in attn_fwd.cu.
+          const float m_prev = m_run;
+          const float mt = fmaxf(half_max(s, 0), half_max(s, 2)) * sl2;
+          const bool resc = mt - m_run > kCacheRescale;   // false while both are -inf
+          if (resc) m_run = mt;
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          const float alpha = resc ? ex2_approx(m_prev - m_run) : 1.f;
+          l_run *= alpha;
+          float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          softmax_chunk(s, 0, sl2, m_use, tS, ls);
+          softmax_chunk(s, 1, sl2, m_use, tS, ls);
+          if (i >= 2 && __any_sync(0xffffffffu, resc)) {
+            // The accumulator holds the products before this tile, all complete.
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+              tmem_st16(tO + c, o);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(smem_addr(&sm.p_full[wg][0]));
+          softmax_chunk(s, 2, sl2, m_use, tS, ls);
+          softmax_chunk(s, 3, sl2, m_use, tS, ls);
+          l_run += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(smem_addr(&sm.p_full[wg][1]));
+        } else {
+          mbar_arrive(smem_addr(&sm.p_full[wg][0]));
+          mbar_arrive(smem_addr(&sm.p_full[wg][1]));
+        }
+      }
+      if (!ok) break;
+      kv += 2 * sg.n;
+      // ---------------------------------------------------------- unit's end
+      const bool two = sg.n > 1;
+      if (wg == 0 || two) {
+        if (!(ok = wait(sm.o_done[wg], od_cnt))) break;
+        ++od_cnt;
+      }
+      sm.ml[wg][row] = make_float2(m_run, l_run);
+      mbar_arrive(smem_addr(&sm.ml_ready));
+      if (!(ok = wait(sm.ml_ready, unit))) break;
+      tc_fence_after();
+      const float2 m0 = sm.ml[0][row], m1 = sm.ml[1][row];
+      const float M = fmaxf(m0.x, m1.x);
+      const float a0 = m0.x == -INFINITY ? 0.f : ex2_approx(m0.x - M);
+      const float a1 = m1.x == -INFINITY ? 0.f : ex2_approx(m1.x - M);
+      const float l = m0.y * a0 + m1.y * a1;
+      const bool whole = sg.n == sg.nt;
+      // A unit cut at this CTA's start goes to its first slot, one cut at its end to the second.
+      float* slot = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (sg.t0 > 0 ? 0 : 1)) * (kTile * (D + 2));
+      const float inv = whole && l > 0.f ? 1.f / l : (whole ? 0.f : 1.f);
+      const int64_t out = (static_cast<int64_t>(sg.b) * p.T + cr.t) * p.Hq + cr.hq;
+      if (busy) {
+#pragma unroll
+        for (int c = wg * (D / 2); c < (wg + 1) * (D / 2); c += 16) {
+          uint32_t x0[16], x1[16];
+          tmem_ld16(tbase + lane_off + 256 + c, x0);
+          if (two) tmem_ld16(tbase + lane_off + 256 + D + c, x1);
+          float y[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            y[q] = __uint_as_float(x0[q]) * a0;
+            if (two) y[q] = fmaf(__uint_as_float(x1[q]), a1, y[q]);
+            y[q] *= inv;
+          }
+          if (cr.valid) {
+            if (!whole || p.o_part != nullptr) {
+              float4* dst = reinterpret_cast<float4*>(whole ? p.o_part + out * D + c : slot + row * D + c);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) dst[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + c);
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                dst[q] = make_uint4(pack_bf16x2(y[8 * q], y[8 * q + 1]), pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                                    pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
+            }
+          }
+        }
+      }
+      if (wg == 0 && cr.valid) {
+        if (whole) store_lse(p, sg.b, cr, l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY);
+        else *reinterpret_cast<float2*>(slot + kTile * D + 2 * row) = make_float2(M, l);
+      }
+      tc_fence_before();
+      mbar_arrive(smem_addr(&sm.unit_done));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Joins the pieces of the units that were cut, one warp per row; writes the rows of
+// sequences without keys (O = 0, lse = -inf) and of those whose length lies outside the
+// cache (NaN).
+template <int D>
+__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheParams p, int row_blocks) {
+  __shared__ int before[kCacheMaxB + 1];
+  __shared__ int warp_sum[8];
+  tile_prefix<256>(p, before, warp_sum);
+  __syncthreads();
+  const int unit = static_cast<int>(blockIdx.x) / row_blocks;
+  const int row = (static_cast<int>(blockIdx.x) % row_blocks) * 8 + static_cast<int>(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int hr = p.Hkv * p.row_tiles;
+  const int b = unit / hr, u = unit - b * hr;
+  const CacheRow cr = cache_row(p, u / p.row_tiles, u % p.row_tiles, row);
+  if (row >= kTile || !cr.valid) return;
+  const int nt = before[b + 1] - before[b];
+  constexpr int kPer = D / 32;
+  float acc[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) acc[q] = 0.f;
+  float lse = -INFINITY, inv = 0.f;
+  if (nt == 0) {
+    if (key_count(p, b) < 0) {
+      lse = __int_as_float(0x7fc00000);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) acc[q] = lse;
+      inv = 1.f;
+    }
+  } else {
+    const int64_t total = static_cast<int64_t>(before[p.B]) * hr;
+    const int64_t first = static_cast<int64_t>(before[b]) * hr + static_cast<int64_t>(u) * nt, last = first + nt - 1;
+    // CTA c holds tiles [total c / n, total (c + 1) / n): the last c whose start is <= f holds f.
+    auto holder = [&](int64_t f) {
+      int64_t c = (f * p.n_cta) / total;
+      while (total * (c + 1) / p.n_cta <= f) ++c;
+      while (total * c / p.n_cta > f) --c;
+      return static_cast<int>(c);
+    };
+    const int c0 = holder(first), c1 = holder(last);
+    if (c0 == c1) return;   // written whole
+    float M = -INFINITY, l = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      if (total * c / p.n_cta == total * (c + 1) / p.n_cta) continue;   // fewer tiles than CTAs: no run
+      const float* slot = p.parts + (2 * static_cast<int64_t>(c) + (total * c / p.n_cta > first ? 0 : 1)) * (kTile * (D + 2));
+      const float2 ml = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * row);
+      if (ml.x == -INFINITY) continue;
+      const float Mn = fmaxf(M, ml.x);
+      const float a = M == -INFINITY ? 0.f : ex2_approx(M - Mn), w = ex2_approx(ml.x - Mn);
+      M = Mn;
+      l = l * a + ml.y * w;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) acc[q] = acc[q] * a + slot[row * D + lane * kPer + q] * w;
+    }
+    inv = l > 0.f ? 1.f / l : 0.f;
+    if (l > 0.f) lse = (M + __log2f(l)) * 0.69314718055994531f;
+  }
+  const int64_t out = ((static_cast<int64_t>(b) * p.T + cr.t) * p.Hq + cr.hq) * D + lane * kPer;
+#pragma unroll
+  for (int q = 0; q < kPer; q += 2) {
+    const float x = acc[q] * inv, y = acc[q + 1] * inv;
+    if (p.o_part != nullptr) *reinterpret_cast<float2*>(p.o_part + out + q) = make_float2(x, y);
+    else *reinterpret_cast<uint32_t*>(p.o + out + q) = pack_bf16x2(x, y);
+  }
+  if (lane == 0) store_lse(p, b, cr, lse);
+}
+
+template <int D>
+bool launch_cache(const CacheLaunch& L, cudaStream_t stream) {
+  const size_t smem = sizeof(CacheSmem<D>) + 1024;
+  auto kern = cache_attn_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return false;
+  kern<<<L.p.n_cta, kCacheThreads, smem, stream>>>(L.tm_q, L.tm_k, L.tm_v, L.p);
+  if (cudaGetLastError() != cudaSuccess) return false;
+  const int rows = L.p.tok_per_tile * L.p.G;
+  const int row_blocks = (rows + 7) / 8;
+  cache_join_kernel<D><<<L.p.B * L.p.Hkv * L.p.row_tiles * row_blocks, 256, 0, stream>>>(L.p, row_blocks);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace
+
+}  // namespace cpattn
+
+using namespace cpattn;
+
+struct cp_cache_plan_s {
+  int B, Hq, Hkv, D, cap, T;
+  float scale;
+  int device = -1, sms = 148;
+  int* d_status = nullptr;
+};
+
+namespace {
+
+// Query tiles: as many whole tokens (G rows each) as fit 128 rows.
+int tokens_per_tile(const cp_cache_plan_s& c) {
+  const int g = c.Hq / c.Hkv;
+  return c.T < kTile / g ? c.T : kTile / g;
+}
+
+size_t cache_workspace(const cp_cache_plan_s& c) {
+  return static_cast<size_t>(2) * c.sms * kTile * (c.D + 2) * sizeof(float);
+}
+
+int run_cache(cp_cache_plan_t plan, const void* q, const void* k, const void* v, const int32_t* lengths, int own,
+              const int64_t* tree, void* o, float* o_part, float* lse, void* workspace, cp_stream_t stream) {
+  if (plan == nullptr || q == nullptr || k == nullptr || v == nullptr || lengths == nullptr ||
+      (o == nullptr && o_part == nullptr))
+    return CP_ERR_INVALID_ARG;
+  if (own != 0 && own != 1) return CP_ERR_INVALID_ARG;
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(o) || !is_aligned16(o_part) ||
+      !is_aligned16(workspace) || (reinterpret_cast<uintptr_t>(lengths) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
+    return CP_ERR_ALIGNMENT;
+  if (workspace == nullptr) return CP_ERR_WORKSPACE;
+  if (plan->d_status == nullptr) return CP_ERR_CUDA;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CP_ERR_CUDA;
+  if (dev != plan->device) return CP_ERR_INVALID_ARG;
+  CacheLaunch L;
+  CacheParams& p = L.p;
+  p.B = plan->B;
+  p.Hq = plan->Hq;
+  p.Hkv = plan->Hkv;
+  p.T = plan->T;
+  p.G = plan->Hq / plan->Hkv;
+  p.cap = plan->cap;
+  p.own = own;
+  p.tok_per_tile = tokens_per_tile(*plan);
+  p.row_tiles = (plan->T + p.tok_per_tile - 1) / p.tok_per_tile;
+  p.n_cta = plan->sms;
+  p.scale_log2 = plan->scale * 1.4426950408889634f;
+  p.lengths = lengths;
+  p.tree = reinterpret_cast<const unsigned long long*>(tree);
+  p.parts = static_cast<float*>(workspace);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_part = o_part;
+  p.lse = lse;
+  p.status = plan->d_status;
+  p.wait_limit_ns = kWaitLimitNs;
+  if (!encode_map_4d(&L.tm_q, q, plan->D, plan->Hq, plan->T, plan->B, p.G, p.tok_per_tile) ||
+      !encode_map_4d(&L.tm_k, k, plan->D, plan->Hkv, plan->cap, plan->B, 1, kTile) ||
+      !encode_map_4d(&L.tm_v, v, plan->D, plan->Hkv, plan->cap, plan->B, 1, kTile))
+    return CP_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return (plan->D == 128 ? launch_cache<128>(L, st) : launch_cache<64>(L, st)) ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cp_cache_plan(cp_cache_plan_t* out, int B, int Hq, int Hkv, int D, int capacity, int T, float softmax_scale) {
+  if (out == nullptr) return CP_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (B < 1 || Hq < 1 || Hkv < 1 || capacity < 1 || T < 1) return CP_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale)) return CP_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return CP_ERR_UNSUPPORTED;
+  if (Hq % Hkv != 0 || Hq / Hkv > kTile || T > kCacheMaxT || B > kCacheMaxB) return CP_ERR_UNSUPPORTED;
+  // Tile counts, row blocks of the join and cache rows are int32.
+  const int64_t tiles = (static_cast<int64_t>(capacity) + kTile - 1) / kTile;
+  if (capacity > (1 << 30) || tiles * B > INT32_MAX || static_cast<int64_t>(B) * Hkv > (1 << 24) || Hq > (1 << 20))
+    return CP_ERR_UNSUPPORTED;
+  const int64_t per_tile = kTile / (Hq / Hkv);
+  if (static_cast<int64_t>(B) * Hkv * ((T + per_tile - 1) / per_tile) * (kTile / 8) > INT32_MAX)
+    return CP_ERR_UNSUPPORTED;
+  cp_cache_plan_s* c = new (std::nothrow) cp_cache_plan_s;
+  if (c == nullptr) return CP_ERR_CUDA;
+  c->B = B;
+  c->Hq = Hq;
+  c->Hkv = Hkv;
+  c->D = D;
+  c->cap = capacity;
+  c->T = T;
+  c->scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(static_cast<float>(D));
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) == cudaSuccess && ndev > 0) {
+    int sms = 0;
+    if (cudaGetDevice(&c->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess || sms <= 0 ||
+        cudaMalloc(&c->d_status, sizeof(int)) != cudaSuccess) {
+      delete c;
+      return CP_ERR_CUDA;
+    }
+    if (cudaMemset(c->d_status, 0, sizeof(int)) != cudaSuccess) {
+      cudaFree(c->d_status);
+      delete c;
+      return CP_ERR_CUDA;
+    }
+    c->sms = sms;
+  }
+  *out = c;
+  return CP_OK;
+}
+
+int cp_cache_plan_destroy(cp_cache_plan_t plan) {
+  if (plan == nullptr) return CP_OK;
+  if (plan->d_status != nullptr) cudaFree(plan->d_status);
+  delete plan;
+  return CP_OK;
+}
+
+size_t cp_cache_attn_workspace_bytes(cp_cache_plan_t plan) { return plan == nullptr ? 0 : cache_workspace(*plan); }
+
+int cp_cache_attn(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache, const int32_t* lengths,
+                  const int64_t* tree, void* o, float* lse, void* workspace, cp_stream_t stream) {
+  if (o == nullptr) return CP_ERR_INVALID_ARG;
+  return run_cache(plan, q, k_cache, v_cache, lengths, 1, tree, o, nullptr, lse, workspace, stream);
+}
+
+int cp_cache_attn_partial(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* lengths, int own_drafts, const int64_t* tree, float* o_part, float* lse_part,
+                          void* workspace, cp_stream_t stream) {
+  if (o_part == nullptr || lse_part == nullptr) return CP_ERR_INVALID_ARG;
+  return run_cache(plan, q, k_cache, v_cache, lengths, own_drafts, tree, nullptr, o_part, lse_part, workspace, stream);
+}
+
+int cp_cache_check(cp_cache_plan_t plan, cp_stream_t stream) {
+  if (plan == nullptr) return CP_ERR_INVALID_ARG;
+  if (plan->d_status == nullptr) return CP_ERR_CUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CP_ERR_CUDA;
+  int status = 0;
+  if (cudaMemcpy(&status, plan->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return CP_ERR_CUDA;
+  if (status != 0) {
+    cudaMemset(plan->d_status, 0, sizeof(int));
+    return status;
+  }
+  return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -503,6 +503,63 @@ CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
 CP_API int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, const void* v,
                            const float* log_decay, float scale, float* state, void* o, cp_stream_t stream);
 
+/*
+ * Attention of T new tokens of each sequence over a key/value cache: the serving form
+ * of cp_attn_fwd. T = 1 decodes; T up to 64 checks a chain or a tree of drafted tokens
+ * at once. The keys and values of the T tokens are already in the cache, at rows
+ * lengths[b] .. lengths[b] + T - 1 after the lengths[b] cached ones. Token t of sequence
+ * b sees cache rows [0, lengths[b]) and row lengths[b] + u iff bit u of tree[b][t] is
+ * set (set bit t for the token itself); query head h reads key/value head
+ * h / (Hq / Hkv). Softmax, scale and lse as in cp_attn_fwd; a row that sees nothing gets
+ * O = 0, lse = -inf. Cache rows from lengths[b] + T on may hold anything.
+ *
+ * A cache plan holds the sizes and a status word: B sequences (<= 1024), Hq query and
+ * Hkv key/value heads (Hq a multiple, at most 128-fold), D 64 or 128, the cache's
+ * capacity in rows, T <= 64, scale <= 0 for 1/sqrt(D). Errors as cp_attn_plan. Calls on
+ * one plan with distinct outputs and workspaces may overlap. Destroy it only when no
+ * launch on it may still run.
+ */
+typedef struct cp_cache_plan_s* cp_cache_plan_t;
+CP_API int cp_cache_plan(cp_cache_plan_t* out, int B, int Hq, int Hkv, int D, int capacity, int T,
+                         float softmax_scale);
+CP_API int cp_cache_plan_destroy(cp_cache_plan_t plan);
+
+/* Workspace bytes of cp_cache_attn and cp_cache_attn_partial. */
+CP_API size_t cp_cache_attn_workspace_bytes(cp_cache_plan_t plan);
+
+/*
+ *   q                : bf16 [B][T][Hq][D], device
+ *   k_cache, v_cache : bf16 [B][capacity][Hkv][D], device
+ *   lengths          : int32 [B], device, 4-byte aligned, 0 <= lengths[b] <= capacity - T;
+ *                      a sequence with another length gets NaN in its O and lse, and no
+ *                      row of the cache is read for it
+ *   tree             : int64 [B][T] bit words, device, 8-byte aligned, bits from T on
+ *                      ignored; NULL for a chain (token t sees drafted tokens 0 .. t)
+ *   o                : bf16 [B][T][Hq][D], device (written)
+ *   lse              : float32 [B][Hq][T], device (written); may be NULL
+ *   workspace        : device, cp_cache_attn_workspace_bytes(plan) bytes
+ * Two kernels on `stream`; nothing is allocated; the values do not depend on timing. The
+ * plan's device must be current (CP_ERR_INVALID_ARG). Waits that run out are reported by
+ * cp_cache_check.
+ */
+CP_API int cp_cache_attn(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* lengths, const int64_t* tree, void* o, float* lse, void* workspace,
+                         cp_stream_t stream);
+
+/*
+ * The partial over one rank's share of a cache that context-parallel ranks divide among
+ * them, for cp_merge_partials: o_part float32 [B*T*Hq][D] (normalised), lse_part float32
+ * [B*T*Hq], row (b*T + t)*Hq + h. own_drafts = 1: the T drafted rows follow this rank's
+ * lengths[b] rows, as above; 0: another rank holds them (lengths[b] <= capacity, tree
+ * unused).
+ */
+CP_API int cp_cache_attn_partial(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* lengths, int own_drafts, const int64_t* tree, float* o_part,
+                                 float* lse_part, void* workspace, cp_stream_t stream);
+
+/* cp_attn_check for a cache plan. */
+CP_API int cp_cache_check(cp_cache_plan_t plan, cp_stream_t stream);
+
 /* Length of the index map written by cp_layout_index_map: B*S for
  * contiguous/zigzag (one entry per token), N*B*S for Ulysses (one entry per
  * (group, batch, token) run of H/N heads). */
