@@ -24,8 +24,9 @@
 // launch (OUT = false) computes each segment's own state, and the second joins those
 // before it at its start.
 //
-// Precision. The state is exact to fp32: the weighted rows of C are split into three
-// bf16 terms (8 + 8 + 8 bits of the fp32 product) multiplied one after the other; the
+// Precision. Where the last state is asked for, the state is exact to fp32: the weighted
+// rows of C are split into three bf16 terms (8 + 8 + 8 bits of the fp32 product) multiplied
+// one after the other; two terms (2^-17) do where it is only read as bf16 operand. The
 // chunk sum starts from zero in TMEM and is added to d^L Z in registers, d^L as an fp32
 // pair, because the tensor core's accumulation truncates and a long run of it would
 // drift. Rounded to bf16: the masked scores (P), and the state where it is multiplied
@@ -54,11 +55,11 @@ constexpr int kPart = 32;            // rows of C weighted and multiplied at a t
 constexpr int kParts = kChunk / kPart;
 constexpr int kPartBlk = kPart * 128;
 
-template <int D, bool OUT>
+template <int D, bool OUT, int TERMS>
 struct LinCfg {
   static constexpr int kBlocks = D / 64;
   static constexpr int kTileBytes = kBlocks * kBlk;       // a 128 x D tile
-  static constexpr int kPerChunk = OUT ? 3 : 2;           // tiles per chunk: B, [A,] C
+  static constexpr int kPerChunk = OUT ? 3 : 2;           // tiles per chunk: C, B[, A]
   static constexpr int kTiles = D == 128 ? (OUT ? 4 : 5) : (OUT ? 9 : 8);
   static constexpr int kThreads = OUT ? 448 : 320;
   static constexpr int kMmaWarp = OUT ? 12 : 8;
@@ -71,41 +72,43 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // A B^T
 __host__ __device__ constexpr uint32_t idesc_kv(int D) { return idesc_bf16_f32(128, D, 1, 1); }   // B^T C (both MN-major)
 __host__ __device__ constexpr uint32_t idesc_y(int D) { return idesc_bf16_f32(128, D, 0, 1); }    // A Z, P C
 
-template <int D, bool OUT>
+template <int D, bool OUT, int TERMS>
 struct alignas(1024) LinSmem {
+  using C = LinCfg<D, OUT, TERMS>;
   // Ring of 128 x D tiles. For D = 64 the state product's upper 64 rows (unused)
   // read the 16 KB after a tile, which stay inside this struct.
-  uint8_t tile[LinCfg<D, OUT>::kTiles][LinCfg<D, OUT>::kTileBytes];
-  uint8_t cs[2][3 * LinCfg<D, OUT>::kTerm];   // weighted C: low, middle, high terms
+  uint8_t tile[C::kTiles][C::kTileBytes];
+  uint8_t cs[2][TERMS * C::kTerm];   // weighted C: low, [middle,] high terms
   uint8_t z[OUT ? D * D * 2 : 1024];          // bf16 state, row = feature of A
-  uint64_t full[LinCfg<D, OUT>::kTiles], empty[LinCfg<D, OUT>::kTiles];
+  uint8_t y[OUT ? 4 : 1][OUT ? 32 * 128 : 1024];   // 32 rows x 64 columns of a warp's output
+  uint64_t full[C::kTiles], empty[C::kTiles];
   uint64_t cs_ready[2], cs_free[2];
   uint64_t s_full, p_ready, kv_done, kv_free, qz_done, z_ready, y_full, y_free, drain;
   alignas(16) float pow32[64];                // [32 + x] = d^x for x = 0 .. 31, 0 below
   uint32_t tmem_base;
   WaitBlock wblk;
 };
-static_assert(sizeof(LinSmem<128, true>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<64, true>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<128, false>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<64, false>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<64, false>::cs) + sizeof(LinSmem<64, false>::z) >= kBlk, "over-read of the last tile");
-static_assert(sizeof(LinSmem<64, true>::cs) + sizeof(LinSmem<64, true>::z) >= kBlk, "over-read of the last tile");
+static_assert(sizeof(LinSmem<128, true, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, true, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<128, false, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, false, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, false, 2>::cs) + sizeof(LinSmem<64, false, 2>::z) >= kBlk, "over-read of the last tile");
+static_assert(sizeof(LinSmem<64, true, 2>::cs) + sizeof(LinSmem<64, true, 2>::z) >= kBlk, "over-read of the last tile");
 
 // Descriptor moved by a byte offset (the address field counts 16-byte units).
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-// 32 bytes of a row; one 32-byte sector per thread where the address allows it.
-__device__ __forceinline__ void st_row32(void* p, const uint32_t* v, bool whole) {
-  if (whole) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
+// TMA store of a box from shared memory, one thread; its own group.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
+// This thread's stores: their sources have been read; they are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // d^n; n = 0 gives 1 also for d = 0.
 __device__ __forceinline__ double decay_pow(double ld, int64_t n) {
@@ -142,16 +145,24 @@ __device__ __forceinline__ int walked_before(const LinParams& p, int ci) {
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-template <int D, bool OUT, bool REV>
-__global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
+// One arrival for a warp whose lanes have all fenced what they publish.
+__device__ __forceinline__ void warp_arrive(uint64_t& bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&bar));
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int D, bool OUT, bool REV, int TERMS>
+__global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     linattn_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ LinParams p) {
-  using C = LinCfg<D, OUT>;
+                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y,
+                   const __grid_constant__ LinParams p) {
+  using C = LinCfg<D, OUT, TERMS>;
   constexpr int NT = C::kTiles;
   constexpr uint32_t kIdescKV = idesc_kv(D), kIdescY = idesc_y(D);
-  constexpr int kTB = 0, kTA = 1, kTC = OUT ? 2 : 1;   // order of a chunk's tiles in the ring
+  constexpr int kTC = 0, kTB = 1, kTA = 2;   // order of a chunk's tiles in the ring: C is weighted ahead
   extern __shared__ uint8_t smem_raw[];
-  LinSmem<D, OUT>& sm = *reinterpret_cast<LinSmem<D, OUT>*>(
+  LinSmem<D, OUT, TERMS>& sm = *reinterpret_cast<LinSmem<D, OUT, TERMS>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -169,17 +180,17 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
       mbar_init(smem_addr(&sm.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_addr(&sm.cs_ready[s]), 256);
+      mbar_init(smem_addr(&sm.cs_ready[s]), 8);
       mbar_init(smem_addr(&sm.cs_free[s]), 1);
     }
     mbar_init(smem_addr(&sm.s_full), 1);
-    mbar_init(smem_addr(&sm.p_ready), 128);
+    mbar_init(smem_addr(&sm.p_ready), 4);
     mbar_init(smem_addr(&sm.kv_done), 1);
-    mbar_init(smem_addr(&sm.kv_free), 256);
+    mbar_init(smem_addr(&sm.kv_free), 8);
     mbar_init(smem_addr(&sm.qz_done), 1);
-    mbar_init(smem_addr(&sm.z_ready), 256);
+    mbar_init(smem_addr(&sm.z_ready), 8);
     mbar_init(smem_addr(&sm.y_full), 1);
-    mbar_init(smem_addr(&sm.y_free), 128);
+    mbar_init(smem_addr(&sm.y_free), 4);
     mbar_init(smem_addr(&sm.drain), 1);
     wait_block_init(sm.wblk, p.status, p.wait_limit_ns);
     fence_barrier_init();
@@ -208,9 +219,21 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
     const uint64_t pol = l2_policy_evict_first();
     bool ok = true;
     int t = 0;
+    // The ring holds little more than a chunk, so the chunk after next is brought into L2
+    // ahead of its loads.
+    auto prefetch = [&](int i) {
+      if (i >= n) return;
+      const ChunkAt c = chunk_at<REV>(p, ci0 + i);
+      for (int which = 0; which < C::kPerChunk; ++which)
+        for (int blk = 0; blk < C::kBlocks; ++blk)
+          tma_prefetch_4d_elect(which == kTB ? &tm_b : which == kTC ? &tm_c : &tm_a, blk * 64, h, c.t0,
+                                c.rank * p.B + b);
+    };
+    prefetch(1);
     for (int i = 0; i < n && ok; ++i) {
       const ChunkAt c = chunk_at<REV>(p, ci0 + i);
       const int rb = c.rank * p.B + b;
+      prefetch(i + 2);
       for (int which = 0; which < C::kPerChunk; ++which, ++t) {
         const int st = t % NT;
         if (t >= NT) ok = all_ok(mbar_wait(smem_addr(&sm.empty[st]), (t / NT - 1) & 1, ctl));
@@ -265,7 +288,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
         tc_fence_after();
         const uint64_t dCs = smem_desc_sw128(smem_addr(&sm.cs[buf][0]), kPartBlk, 1024);
 #pragma unroll
-        for (int term = 0; term < 3; ++term)
+        for (int term = 0; term < TERMS; ++term)
 #pragma unroll
           for (int kk = 0; kk < kPart / 16; ++kk)
             umma_ss_elect(tbase, desc_at(dBt, part * kPartBlk + kk * 2048), desc_at(dCs, term * C::kTerm + kk * 2048),
@@ -312,6 +335,9 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
 #pragma unroll
     for (int q = 0; q < D / 2; ++q) z[q] = 0.f;
     const int64_t state0 = static_cast<int64_t>(bh) * D * D;
+    // A segment's own state is kept in the order the threads hold it: vector q of (half, row) at
+    // q * 2D + half * D + row, so that a warp's accesses are contiguous.
+    const int zt = (warp >> 2) * D + row;
     if (OUT && live) {
       const int x = walked_before<REV>(p, ci0);
       if (p.z0 != nullptr) {
@@ -324,12 +350,12 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
       }
       for (int g = 0; g < seg; ++g) {
         const int end = walked_before<REV>(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
-        const float w = static_cast<float>(decay_pow(ld, x - end));
+        const float w = x == end ? 1.f : expf(static_cast<float>(ld * (x - end)));
         const float4* src = reinterpret_cast<const float4*>(
-            p.zseg + ((static_cast<int64_t>(bh) * (p.nseg - 1) + g) * D + row) * D + col0);
+                                p.zseg + (static_cast<int64_t>(bh) * (p.nseg - 1) + g) * (D * D)) + zt;
 #pragma unroll
         for (int q = 0; q < D / 8; ++q) {
-          const float4 v = src[q];
+          const float4 v = src[q * (2 * D)];
           z[4 * q] = fmaf(w, v.x, z[4 * q]);
           z[4 * q + 1] = fmaf(w, v.y, z[4 * q + 1]);
           z[4 * q + 2] = fmaf(w, v.z, z[4 * q + 2]);
@@ -347,54 +373,57 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
                          pack_bf16x2(z[8 * v + 4], z[8 * v + 5]), pack_bf16x2(z[8 * v + 6], z[8 * v + 7]));
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(smem_addr(&sm.z_ready));
+      fence_async_smem();
+      warp_arrive(sm.z_ready);
     };
     if constexpr (OUT) publish();
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
+    // Weights rows [32 part, 32 part + 32) of chunk i into their buffer.
+    auto weight = [&](int i, int part) {
       const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
-      const int tC = i * C::kPerChunk + kTC;
-      if (!(ok = tile_full(tC))) break;
-      const uint8_t* src = &sm.tile[tC % NT][0];
+      const int tC = i * C::kPerChunk + kTC, buf = part & 1, use = (i * kParts + part) >> 1;
+      if (part == 0 && !tile_full(tC)) return false;
+      if (use > 0 && !all_ok(mbar_wait(smem_addr(&sm.cs_free[buf]), (use - 1) & 1, ctl))) return false;
+      const uint8_t* src = &sm.tile[tC % NT][part * kPartBlk];
+      const float w = whole ? w_full[part] : w_tail[part];
+      const bool keep = whole || part * kPart + crow < tail;   // other rows may follow in memory
+      const int swz = crow * 128 + ((cvec ^ (crow & 7)) * 16);
 #pragma unroll
-      for (int part = 0; part < kParts; ++part) {
-        const int buf = part & 1, use = (i * kParts + part) >> 1;
-        if (use > 0 && !(ok = all_ok(mbar_wait(smem_addr(&sm.cs_free[buf]), (use - 1) & 1, ctl)))) break;
-        const float w = whole ? w_full[part] : w_tail[part];
-        const bool keep = whole || part * kPart + crow < tail;   // other rows may follow in memory
-        const int swz = crow * 128 + ((cvec ^ (crow & 7)) * 16);
+      for (int blk = 0; blk < C::kBlocks; ++blk) {
+        uint4 v = *reinterpret_cast<const uint4*>(src + blk * kBlk + swz);
+        if (!keep) v = make_uint4(0, 0, 0, 0);
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t t[3][4];   // high, middle, low
+        const uint64_t ww = f2_pack(w, w);
 #pragma unroll
-        for (int blk = 0; blk < C::kBlocks; ++blk) {
-          uint4 v = *reinterpret_cast<const uint4*>(src + blk * kBlk + part * kPartBlk + swz);
-          if (!keep) v = make_uint4(0, 0, 0, 0);
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t t0[4], t1[4], t2[4];
-          const uint64_t ww = f2_pack(w, w);
+        for (int q = 0; q < 4; ++q) {
+          uint64_t x = f2_mul(bf16x2_to_f2(in[q]), ww);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int k = 0; k < TERMS; ++k) {
             float x0, x1;
-            const uint64_t x = f2_mul(bf16x2_to_f2(in[q]), ww);
             f2_unpack(x, x0, x1);
-            t0[q] = pack_bf16x2(x0, x1);
-            const uint64_t r = f2_sub(x, bf16x2_to_f2(t0[q]));
-            f2_unpack(r, x0, x1);
-            t1[q] = pack_bf16x2(x0, x1);
-            f2_unpack(f2_sub(r, bf16x2_to_f2(t1[q])), x0, x1);
-            t2[q] = pack_bf16x2(x0, x1);
+            t[k][q] = pack_bf16x2(x0, x1);
+            if (k + 1 < TERMS) x = f2_sub(x, bf16x2_to_f2(t[k][q]));
           }
-          uint8_t* dst = &sm.cs[buf][blk * kPartBlk + swz];
-          *reinterpret_cast<uint4*>(dst) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-          *reinterpret_cast<uint4*>(dst + C::kTerm) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-          *reinterpret_cast<uint4*>(dst + 2 * C::kTerm) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(smem_addr(&sm.cs_ready[buf]));
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+          *reinterpret_cast<uint4*>(&sm.cs[buf][(TERMS - 1 - k) * C::kTerm + blk * kPartBlk + swz]) =
+              make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
       }
-      if (!ok) break;
+      fence_async_smem();
+      warp_arrive(sm.cs_ready[buf]);
+      return true;
+    };
+    // The first two parts of a chunk are weighted before the state of the chunk before is
+    // taken, while the tensor core finishes it.
+    ok = n == 0 || (weight(0, 0) && weight(0, 1));
+    for (int i = 0; i < n && ok; ++i) {
+      if (!(ok = weight(i, 2) && weight(i, 3))) break;
+      if (i + 1 < n && !(ok = weight(i + 1, 0) && weight(i + 1, 1))) break;
       if (!(ok = all_ok(mbar_wait(smem_addr(&sm.kv_done), i & 1, ctl)))) break;
       tc_fence_after();
-      const double dl = whole ? d_full : d_tail;
+      const double dl = chunk_at<REV>(p, ci0 + i).len == kChunk ? d_full : d_tail;
       const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
       if (quad * 32 < D) {
 #pragma unroll
@@ -407,24 +436,20 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
       }
       tc_fence_before();
       if (i + 1 < n) {
-        mbar_arrive(smem_addr(&sm.kv_free));
+        warp_arrive(sm.kv_free);
         if constexpr (OUT) {
           if (!(ok = all_ok(mbar_wait(smem_addr(&sm.qz_done), i & 1, ctl)))) break;
           publish();
         }
       }
     }
-    if (ok && live) {
-      float* dst = nullptr;
-      if (!OUT)
-        dst = p.zseg + ((static_cast<int64_t>(bh) * (p.nseg - 1) + seg) * D + row) * D + col0;
-      else if (seg == p.nseg - 1 && p.z_out != nullptr)
-        dst = p.z_out + state0 + row * D + col0;
-      if (dst != nullptr) {
+    if (ok && live && (!OUT || (seg == p.nseg - 1 && p.z_out != nullptr))) {
+      float4* dst = reinterpret_cast<float4*>(
+          OUT ? p.z_out + state0 + row * D + col0
+              : p.zseg + (static_cast<int64_t>(bh) * (p.nseg - 1) + seg) * (D * D)) + (OUT ? 0 : zt);
 #pragma unroll
-        for (int q = 0; q < D / 8; ++q)
-          reinterpret_cast<float4*>(dst)[q] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
-      }
+      for (int q = 0; q < D / 8; ++q)
+        dst[q * (OUT ? 1 : 2 * D)] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
     }
   } else if (OUT && warp < 12) {
     // --------------------------------- masked scores and output, one row per lane
@@ -432,7 +457,6 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const float ldf = static_cast<float>(ld);
-    const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31u) == 0;
     // Decay of score (row, 32m + jj), exponent |row - column| >= 0: off the diagonal block
     // (m != quad) a row factor times a column power, forward d^(row - 32m - 31) d^(31 - jj),
     // backward d^(32m - row) d^jj; on it d^|lane - jj| from the table.
@@ -486,32 +510,53 @@ __global__ void __launch_bounds__(LinCfg<D, OUT>::kThreads, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(smem_addr(&sm.p_ready));
+      warp_arrive(sm.p_ready);
       const int x = REV ? c.len - 1 - row : row + 1;
       const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
       const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
       __nv_bfloat16* dst = p.y + (tok * p.H + h) * D;
       if (!(ok = all_ok(mbar_wait(smem_addr(&sm.y_full), i & 1, ctl)))) break;
       tc_fence_after();
+      // Through shared memory and a TMA store, 64 columns at a time; a warp whose rows
+      // end inside the chunk stores them itself (the rows after may be another rank's).
+      const bool staged = quad * 32 + 32 <= c.len;
 #pragma unroll
-      for (int q = 0; q < D; q += 32) {
-        uint32_t az[32], pc[32], out[16];
-        tmem_ld32(tAZ + lane_off + q, az);
-        tmem_ld32(tPC + lane_off + q, pc);
+      for (int half = 0; half < C::kBlocks; ++half) {
+        uint32_t out[32];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          out[k] = pack_bf16x2(fmaf(__uint_as_float(az[2 * k]), w, __uint_as_float(pc[2 * k])),
-                               fmaf(__uint_as_float(az[2 * k + 1]), w, __uint_as_float(pc[2 * k + 1])));
-        if (q + 32 == D) {
-          tc_fence_before();
-          mbar_arrive(smem_addr(&sm.y_free));
+        for (int q = 0; q < 64; q += 16) {
+          uint32_t az[16], pc[16];
+          tmem_ld16(tAZ + lane_off + half * 64 + q, az);
+          tmem_ld16(tPC + lane_off + half * 64 + q, pc);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            out[q / 2 + k] = pack_bf16x2(fmaf(__uint_as_float(az[2 * k]), w, __uint_as_float(pc[2 * k])),
+                                         fmaf(__uint_as_float(az[2 * k + 1]), w, __uint_as_float(pc[2 * k + 1])));
         }
-        if (row < c.len) {
-          st_row32(dst + q, out, wide);
-          st_row32(dst + q + 16, out + 8, wide);
+        if (half + 1 == C::kBlocks) {
+          tc_fence_before();
+          warp_arrive(sm.y_free);
+        }
+        if (staged) {
+          if (lane == 0) bulk_wait_read();   // the store before has left the buffer
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(&sm.y[quad][lane * 128 + ((k ^ (lane & 7)) * 16)]) =
+                make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            tma_store_4d(&tm_y, smem_addr(&sm.y[quad][0]), half * 64, h, c.t0 + quad * 32, c.rank * p.B + b);
+        } else if (row < c.len) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4*>(dst + half * 64)[k] =
+                make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -591,23 +636,28 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
   for (int r = 0; r < RPT; ++r) *reinterpret_cast<float4*>(st + static_cast<int64_t>(rg + r * RG) * D) = s[r];
 }
 
-template <int D, bool OUT, bool REV>
+template <int D, bool OUT, bool REV, int TERMS>
 cudaError_t launch_lin(const LinLaunch& L, int grid, cudaStream_t stream) {
-  const size_t smem = sizeof(LinSmem<D, OUT>) + 1024;
-  auto kern = linattn_kernel<D, OUT, REV>;
+  const size_t smem = sizeof(LinSmem<D, OUT, TERMS>) + 1024;
+  auto kern = linattn_kernel<D, OUT, REV, TERMS>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<grid, LinCfg<D, OUT>::kThreads, smem, stream>>>(L.tm_a, L.tm_b, L.tm_c, L.p);
+  kern<<<grid, LinCfg<D, OUT, TERMS>::kThreads, smem, stream>>>(L.tm_a, L.tm_b, L.tm_c, L.tm_y, L.p);
   return cudaGetLastError();
 }
 
 // The launches of one scan: the segments' own states (all but the last), then the rows.
-template <int D, bool REV>
+template <int D, bool REV, int TERMS>
 bool launch_scan(const LinLaunch& L, cudaStream_t stream) {
   const LinParams& p = L.p;
-  if (p.nseg > 1 && launch_lin<D, false, REV>(L, p.units * (p.nseg - 1), stream) != cudaSuccess) return false;
-  return launch_lin<D, true, REV>(L, p.units * p.nseg, stream) == cudaSuccess;
+  if (p.nseg > 1 && launch_lin<D, false, REV, TERMS>(L, p.units * (p.nseg - 1), stream) != cudaSuccess) return false;
+  return launch_lin<D, true, REV, TERMS>(L, p.units * p.nseg, stream) == cudaSuccess;
+}
+template <int D>
+bool launch_scan(const LinLaunch& L, cudaStream_t stream) {
+  if (L.p.z_out != nullptr) return L.p.reverse ? launch_scan<D, true, 3>(L, stream) : launch_scan<D, false, 3>(L, stream);
+  return L.p.reverse ? launch_scan<D, true, 2>(L, stream) : launch_scan<D, false, 2>(L, stream);
 }
 
 // ------------------------------------------------------------------------ host side
@@ -675,7 +725,8 @@ int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float
   const int64_t rb = static_cast<int64_t>(w.N) * v.B;
   if (!encode_map_4d(&L.tm_a, s.a, v.D, v.H, w.T, rb, 1, kChunk) ||
       !encode_map_4d(&L.tm_b, s.b, v.D, v.H, w.T, rb, 1, kChunk) ||
-      !encode_map_4d(&L.tm_c, s.c, v.D, v.H, w.T, rb, 1, kChunk))
+      !encode_map_4d(&L.tm_c, s.c, v.D, v.H, w.T, rb, 1, kChunk) ||
+      !encode_map_4d(&L.tm_y, s.y, v.D, v.H, w.T, rb, 1, 32))
     return CP_ERR_CUDA;
   LinParams& p = L.p;
   p.B = v.B;
@@ -701,8 +752,7 @@ int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float
   p.y = static_cast<__nv_bfloat16*>(s.y);
   p.status = v.status;
   p.wait_limit_ns = kWaitLimitNs;
-  const bool ok = v.D == 128 ? (s.reverse ? launch_scan<128, true>(L, stream) : launch_scan<128, false>(L, stream))
-                             : (s.reverse ? launch_scan<64, true>(L, stream) : launch_scan<64, false>(L, stream));
+  const bool ok = v.D == 128 ? launch_scan<128>(L, stream) : launch_scan<64>(L, stream);
   return ok ? CP_OK : CP_ERR_CUDA;
 }
 

@@ -30,7 +30,7 @@ struct LinParams {
 };
 
 struct LinLaunch {
-  CUtensorMap tm_a, tm_b, tm_c;   // 4-D views (D, H, T, N*B)
+  CUtensorMap tm_a, tm_b, tm_c, tm_y;   // 4-D views (D, H, T, N*B)
   LinParams p;
 };
 

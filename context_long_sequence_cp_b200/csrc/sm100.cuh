@@ -205,6 +205,17 @@ __device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMa
       : "memory");
 }
 
+// The same tile brought into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d_elect(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n\t}" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 // Untiled bulk copy global -> shared (both 16-byte aligned, bytes a multiple of
 // 16), completion as transaction bytes on an mbarrier; issued by one elected
 // lane of a converged warp. No multicast.
