@@ -51,52 +51,68 @@ namespace {
 
 constexpr int kChunk = 128;          // tokens of a chunk: the 128 lanes of a tcgen05 product
 constexpr int kBlk = kChunk * 128;   // 128 rows x 128 B: one swizzled 64-column block
-constexpr int kPart = 32;            // rows of C weighted and multiplied at a time
-constexpr int kParts = kChunk / kPart;
-constexpr int kPartBlk = kPart * 128;
+constexpr int kHalf = kChunk / 2;    // tokens of C that one group of four warps weights
 
 template <int D, bool OUT, int TERMS>
 struct LinCfg {
   static constexpr int kBlocks = D / 64;
   static constexpr int kTileBytes = kBlocks * kBlk;       // a 128 x D tile
-  static constexpr int kPerChunk = OUT ? 3 : 2;           // tiles per chunk: C, B[, A]
-  static constexpr int kTiles = D == 128 ? (OUT ? 4 : 5) : (OUT ? 9 : 8);
+  static constexpr int kPerChunk = OUT ? 3 : 2;           // tiles per chunk: [A,] B, C
+  static constexpr int kTiles = D == 128 ? (OUT ? 5 : 6) : (OUT ? 9 : 10);
   static constexpr int kThreads = OUT ? 448 : 320;
   static constexpr int kMmaWarp = OUT ? 12 : 8;
-  static constexpr int kTerm = kBlocks * kPartBlk;        // one term of a part of weighted C
-  // TMEM columns: chunk state [0,128), and with OUT the scores/P [128,256),
-  // A Z [256,384), P C [384,512).
-  static constexpr int kTmemCols = OUT ? 512 : 128;
+  // Tokens a group weights at a time, so that the terms of both groups fit 128 columns.
+  static constexpr int kStep = TERMS == 3 ? 32 : 64;
+  static constexpr int kSteps = kHalf / kStep;
+  // TMEM columns: chunk state, transposed [0,128); weighted C^T [128,256), a group's
+  // terms side by side in bf16 pairs; with OUT the scores/P [256,384) and the output
+  // [384,512).
+  static constexpr int kTmemCols = OUT ? 512 : 256;
+  static constexpr int kGroupCols = TERMS * kStep / 2;
 };
+constexpr int kColCw = 128, kColS = 256, kColY = 384;
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // A B^T
-__host__ __device__ constexpr uint32_t idesc_kv(int D) { return idesc_bf16_f32(128, D, 1, 1); }   // B^T C (both MN-major)
-__host__ __device__ constexpr uint32_t idesc_y(int D) { return idesc_bf16_f32(128, D, 0, 1); }    // A Z, P C
+// A Z: both operands K-major. C^T B and P C: left operand in TMEM, right MN-major.
+__host__ __device__ constexpr uint32_t idesc_az(int D) { return idesc_bf16_f32(128, D, 0, 0); }
+__host__ __device__ constexpr uint32_t idesc_ts(int D) { return idesc_bf16_f32(128, D, 0, 1); }
 
 template <int D, bool OUT, int TERMS>
 struct alignas(1024) LinSmem {
   using C = LinCfg<D, OUT, TERMS>;
-  // Ring of 128 x D tiles. For D = 64 the state product's upper 64 rows (unused)
-  // read the 16 KB after a tile, which stay inside this struct.
-  uint8_t tile[C::kTiles][C::kTileBytes];
-  uint8_t cs[2][TERMS * C::kTerm];   // weighted C: low, [middle,] high terms
-  uint8_t z[OUT ? D * D * 2 : 1024];          // bf16 state, row = feature of A
-  uint8_t y[OUT ? 4 : 1][OUT ? 32 * 128 : 1024];   // 32 rows x 64 columns of a warp's output
+  uint8_t tile[C::kTiles][C::kTileBytes];            // ring of 128 x D tiles
+  uint8_t z[OUT ? D * D * 2 : 1024];                 // bf16 Z^T: row = feature of C, 64-column blocks
+  uint8_t y[OUT ? D / 64 : 1][OUT ? 4 : 1][OUT ? 32 * 128 : 1024];   // output: 32 rows x 64 columns per warp
   uint64_t full[C::kTiles], empty[C::kTiles];
-  uint64_t cs_ready[2], cs_free[2];
-  uint64_t s_full, p_ready, kv_done, kv_free, qz_done, z_ready, y_full, y_free, drain;
-  alignas(16) float pow32[64];                // [32 + x] = d^x for x = 0 .. 31, 0 below
+  uint64_t cw_ready[2], cw_free[2];                  // per group of weighting warps
+  uint64_t s_full, p_ready, kv_done, kv_free, az_done, z_ready, y_full, y_free, drain;
+  alignas(16) float pow32[64];                       // [32 + x] = d^x for x = 0 .. 31, 0 below
+  float2 w_full[kChunk / 2], w_tail[kChunk / 2];     // weights of the rows of C, of a whole and of a tail chunk
   uint32_t tmem_base;
   WaitBlock wblk;
 };
-static_assert(sizeof(LinSmem<128, true, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<64, true, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<128, false, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<64, false, 3>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
-static_assert(sizeof(LinSmem<64, false, 2>::cs) + sizeof(LinSmem<64, false, 2>::z) >= kBlk, "over-read of the last tile");
-static_assert(sizeof(LinSmem<64, true, 2>::cs) + sizeof(LinSmem<64, true, 2>::z) >= kBlk, "over-read of the last tile");
+static_assert(sizeof(LinSmem<128, true, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, true, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<128, false, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+static_assert(sizeof(LinSmem<64, false, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
 
 // Descriptor moved by a byte offset (the address field counts 16-byte units).
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// Four transposed 8 x 8 bf16 matrices: matrix m's rows (16 bytes) are at the addresses of
+// lanes 8m .. 8m + 7; lane t gets column t / 4, rows 2 (t % 4) and the next.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes x 8 columns of TMEM from two pairs of such fragments: registers 2k and 2k + 1
+// hold lanes t / 4 and 8 + t / 4 of column 4k + t % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
+}
 
 // TMA store of a box from shared memory, one thread; its own group.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
@@ -106,8 +122,11 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t sr
       "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
-// This thread's stores: their sources have been read; they are complete.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// This thread's stores: the sources of all but the newest N groups have been read; all are complete.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // d^n; n = 0 gives 1 also for d = 0.
@@ -159,8 +178,9 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
                    const __grid_constant__ LinParams p) {
   using C = LinCfg<D, OUT, TERMS>;
   constexpr int NT = C::kTiles;
-  constexpr uint32_t kIdescKV = idesc_kv(D), kIdescY = idesc_y(D);
-  constexpr int kTC = 0, kTB = 1, kTA = 2;   // order of a chunk's tiles in the ring: C is weighted ahead
+  // Order of a chunk's tiles in the ring: A is the first to be free, so the next chunk's A and B
+  // load while this one is multiplied.
+  constexpr int kTA = 0, kTB = OUT ? 1 : 0, kTC = OUT ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   LinSmem<D, OUT, TERMS>& sm = *reinterpret_cast<LinSmem<D, OUT, TERMS>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -173,6 +193,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   const int ci1 = static_cast<int>(static_cast<int64_t>(seg + 1) * p.nch / p.nseg);
   const int n = ci1 - ci0;
   const double ld = static_cast<double>(__ldg(p.log_decay + h));
+  const int tail = p.piece_len % kChunk;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NT; ++s) {
@@ -180,14 +201,14 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       mbar_init(smem_addr(&sm.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_addr(&sm.cs_ready[s]), 8);
-      mbar_init(smem_addr(&sm.cs_free[s]), 1);
+      mbar_init(smem_addr(&sm.cw_ready[s]), 4);
+      mbar_init(smem_addr(&sm.cw_free[s]), 1);
     }
     mbar_init(smem_addr(&sm.s_full), 1);
     mbar_init(smem_addr(&sm.p_ready), 4);
     mbar_init(smem_addr(&sm.kv_done), 1);
     mbar_init(smem_addr(&sm.kv_free), 8);
-    mbar_init(smem_addr(&sm.qz_done), 1);
+    mbar_init(smem_addr(&sm.az_done), 1);
     mbar_init(smem_addr(&sm.z_ready), 8);
     mbar_init(smem_addr(&sm.y_full), 1);
     mbar_init(smem_addr(&sm.y_free), 4);
@@ -197,6 +218,11 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   }
   if (threadIdx.x < 64)
     sm.pow32[threadIdx.x] = threadIdx.x < 32 ? 0.f : static_cast<float>(decay_pow(ld, threadIdx.x - 32));
+  if (threadIdx.x < 256) {
+    const int r = threadIdx.x & 127, len = threadIdx.x < 128 ? kChunk : tail;
+    const float w = r < len ? static_cast<float>(decay_pow(ld, REV ? r + 1 : len - 1 - r)) * p.s_upd : 0.f;
+    reinterpret_cast<float*>(threadIdx.x < 128 ? sm.w_full : sm.w_tail)[r] = w;
+  }
   if (warp == C::kMmaWarp) {
     tmem_alloc(smem_addr(&sm.tmem_base), C::kTmemCols);
     tmem_relinquish();
@@ -211,22 +237,22 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl ctl = wait_ctl(sm.wblk);
-  const uint32_t tS = tbase + 128, tAZ = tbase + 256, tPC = tbase + 384;
-  auto tile_full = [&](int t) { return all_ok(mbar_wait(smem_addr(&sm.full[t % NT]), (t / NT) & 1, ctl)); };
+  const uint32_t tCw = tbase + kColCw, tS = tbase + kColS, tY = tbase + kColY;
+  auto wait = [&](uint64_t& bar, int phase) { return all_ok(mbar_wait(smem_addr(&bar), phase & 1, ctl)); };
+  auto tile_full = [&](int t) { return wait(sm.full[t % NT], t / NT); };
 
   if (warp == C::kMmaWarp + 1) {
     // ---------------------------------------------------------------- TMA
     const uint64_t pol = l2_policy_evict_first();
     bool ok = true;
     int t = 0;
-    // The ring holds little more than a chunk, so the chunk after next is brought into L2
-    // ahead of its loads.
+    // The ring holds less than two chunks, so the one after next is brought into L2 ahead.
     auto prefetch = [&](int i) {
       if (i >= n) return;
       const ChunkAt c = chunk_at<REV>(p, ci0 + i);
       for (int which = 0; which < C::kPerChunk; ++which)
         for (int blk = 0; blk < C::kBlocks; ++blk)
-          tma_prefetch_4d_elect(which == kTB ? &tm_b : which == kTC ? &tm_c : &tm_a, blk * 64, h, c.t0,
+          tma_prefetch_4d_elect(which == kTC ? &tm_c : which == kTB ? &tm_b : &tm_a, blk * 64, h, c.t0,
                                 c.rank * p.B + b);
     };
     prefetch(1);
@@ -236,10 +262,9 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       prefetch(i + 2);
       for (int which = 0; which < C::kPerChunk; ++which, ++t) {
         const int st = t % NT;
-        if (t >= NT) ok = all_ok(mbar_wait(smem_addr(&sm.empty[st]), (t / NT - 1) & 1, ctl));
-        if (!ok) break;
+        if (t >= NT && !(ok = wait(sm.empty[st], t / NT - 1))) break;
         const uint32_t bar = smem_addr(&sm.full[st]);
-        const CUtensorMap* map = which == kTB ? &tm_b : which == kTC ? &tm_c : &tm_a;
+        const CUtensorMap* map = which == kTC ? &tm_c : which == kTB ? &tm_b : &tm_a;
         mbar_arrive_expect_tx_elect(bar, C::kTileBytes);
         for (int blk = 0; blk < C::kBlocks; ++blk)
           tma_load_4d_elect(smem_addr(&sm.tile[st][0]) + blk * kBlk, map, bar, blk * 64, h, c.t0, rb, pol);
@@ -250,11 +275,12 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         if (k >= 0) mbar_wait_drain(smem_addr(&sm.full[k % NT]), (k / NT) & 1, p.wait_limit_ns);
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA
-    const uint64_t d_z = smem_desc_sw128(smem_addr(&sm.z[0]), D * 128, 1024);
+    constexpr uint32_t kIdescAZ = idesc_az(D), kIdescTS = idesc_ts(D);
+    const uint64_t dZ = smem_desc_sw128(smem_addr(&sm.z[0]), 16, 1024);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int tB = i * C::kPerChunk + kTB, tA = i * C::kPerChunk + kTA, tC = i * C::kPerChunk + kTC;
-      const uint32_t aB = smem_addr(&sm.tile[tB % NT][0]), aA = smem_addr(&sm.tile[tA % NT][0]),
+      const int tA = i * C::kPerChunk + kTA, tB = i * C::kPerChunk + kTB, tC = i * C::kPerChunk + kTC;
+      const uint32_t aA = smem_addr(&sm.tile[tA % NT][0]), aB = smem_addr(&sm.tile[tB % NT][0]),
                      aC = smem_addr(&sm.tile[tC % NT][0]);
       if (!(ok = tile_full(tB))) break;
       if constexpr (OUT) {
@@ -269,43 +295,43 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         }
         umma_commit_elect(smem_addr(&sm.s_full));
         // A Z, onto the columns the output warps have read for the previous chunk.
-        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.z_ready), i & 1, ctl)))) break;
-        if (i > 0 && !(ok = all_ok(mbar_wait(smem_addr(&sm.y_free), (i - 1) & 1, ctl)))) break;
+        if (!(ok = wait(sm.z_ready, i))) break;
+        if (i > 0 && !(ok = wait(sm.y_free, i - 1))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_elect(tAZ, desc_at(dA, (kk >> 2) * kBlk + (kk & 3) * 32), desc_at(d_z, kk * 2048), kIdescY,
-                        kk > 0);
-        umma_commit_elect(smem_addr(&sm.qz_done));
+          umma_ss_elect(tY, desc_at(dA, (kk >> 2) * kBlk + (kk & 3) * 32),
+                        desc_at(dZ, (kk >> 2) * (D * 128) + (kk & 3) * 32), kIdescAZ, kk > 0);
+        umma_commit_elect(smem_addr(&sm.az_done));
         umma_commit_elect(smem_addr(&sm.empty[tA % NT]));
       }
-      // Chunk state, part by part as the weighted rows of C come, smallest term first.
-      if (i > 0 && !(ok = all_ok(mbar_wait(smem_addr(&sm.kv_free), (i - 1) & 1, ctl)))) break;
-      const uint64_t dBt = smem_desc_sw128(aB, kBlk, 1024);
-      for (int part = 0; part < kParts; ++part) {
-        const int buf = part & 1, use = (i * kParts + part) >> 1;
-        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.cs_ready[buf]), use & 1, ctl)))) break;
+      // Chunk state, as the weighted rows of C come, smallest term first.
+      if (i > 0 && !(ok = wait(sm.kv_free, i - 1))) break;
+      const uint64_t dBn = smem_desc_sw128(aB, kBlk, 1024);
+      for (int part = 0; part < 2 * C::kSteps; ++part) {
+        const int g = part & 1, step = part >> 1;
+        if (!(ok = wait(sm.cw_ready[g], i * C::kSteps + step))) break;
         tc_fence_after();
-        const uint64_t dCs = smem_desc_sw128(smem_addr(&sm.cs[buf][0]), kPartBlk, 1024);
+        const uint64_t d = desc_at(dBn, (g * kHalf + step * C::kStep) * 128);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-          for (int kk = 0; kk < kPart / 16; ++kk)
-            umma_ss_elect(tbase, desc_at(dBt, part * kPartBlk + kk * 2048), desc_at(dCs, term * C::kTerm + kk * 2048),
-                          kIdescKV, part > 0 || term > 0 || kk > 0);
-        umma_commit_elect(smem_addr(&sm.cs_free[buf]));
+          for (int kk = 0; kk < C::kStep / 16; ++kk)
+            umma_ts_elect(tbase, tCw + g * C::kGroupCols + term * (C::kStep / 2) + kk * 8, desc_at(d, kk * 2048),
+                          kIdescTS, part > 0 || term > 0 || kk > 0);
+        umma_commit_elect(smem_addr(&sm.cw_free[g]));
       }
       if (!ok) break;
       umma_commit_elect(smem_addr(&sm.kv_done));
       umma_commit_elect(smem_addr(&sm.empty[tB % NT]));
       if constexpr (OUT) {
         if (!(ok = tile_full(tC))) break;
-        if (!(ok = all_ok(mbar_wait(smem_addr(&sm.p_ready), i & 1, ctl)))) break;
+        if (!(ok = wait(sm.p_ready, i))) break;   // P written, and A Z scaled: P C adds to it
         tc_fence_after();
         const uint64_t dC = smem_desc_sw128(aC, kBlk, 1024);
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
-          umma_ts_elect(tPC, tS + kk * 8, desc_at(dC, kk * 2048), kIdescY, kk > 0);
+          umma_ts_elect(tY, tS + kk * 8, desc_at(dC, kk * 2048), kIdescTS, 1u);
         umma_commit_elect(smem_addr(&sm.y_full));
       }
       umma_commit_elect(smem_addr(&sm.empty[tC % NT]));
@@ -315,37 +341,28 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       mbar_wait_drain(smem_addr(&sm.drain), 0, p.wait_limit_ns);
     }
   } else if (warp < 8) {
-    // ------------------------------------ weighted C in three bf16 terms, and the state
-    const int crow = threadIdx.x >> 3, cvec = threadIdx.x & 7;   // row of a part, 16-byte vector of a block
-    const int quad = warp & 3;
-    const int row = quad * 32 + lane;          // feature of B (row of Z)
-    const int col0 = (warp >> 2) * (D / 2);    // columns of Z held by this thread
-    const bool live = row < D;
-    const uint32_t tKV = tbase + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-    const int tail = p.piece_len % kChunk;
-    float w_full[kParts], w_tail[kParts];      // weights of this thread's rows of C, 0 past a tail chunk's tokens
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) {
-      const int r = part * kPart + crow;
-      w_full[part] = static_cast<float>(decay_pow(ld, REV ? r + 1 : kChunk - 1 - r)) * p.s_upd;
-      w_tail[part] = r < tail ? static_cast<float>(decay_pow(ld, REV ? r + 1 : tail - 1 - r)) * p.s_upd : 0.f;
-    }
+    // ---------------------- weighted C^T in bf16 terms, and the state; lanes are features of C
+    const int quad = warp & 3, grp = warp >> 2;
+    const int row = quad * 32 + lane;          // feature of C (column of Z)
+    const int col0 = grp * (D / 2);            // features of B (rows of Z) held by this thread
+    const bool busy = quad * 32 < D;           // warp-uniform; for D = 64 two quads have no rows
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const double d_full = decay_pow(ld, kChunk), d_tail = decay_pow(ld, tail);
     float z[D / 2];
 #pragma unroll
     for (int q = 0; q < D / 2; ++q) z[q] = 0.f;
     const int64_t state0 = static_cast<int64_t>(bh) * D * D;
-    // A segment's own state is kept in the order the threads hold it: vector q of (half, row) at
-    // q * 2D + half * D + row, so that a warp's accesses are contiguous.
-    const int zt = (warp >> 2) * D + row;
-    if (OUT && live) {
+    // A segment's own state is kept in the order the threads hold it: vector q of (group, row) at
+    // q * 2D + group * D + row, so that a warp's accesses are contiguous.
+    const int zt = grp * D + row;
+    if (OUT && busy) {
       const int x = walked_before<REV>(p, ci0);
       if (p.z0 != nullptr) {
         const float w = static_cast<float>(decay_pow(ld, x));
 #pragma unroll
         for (int q = 0; q < D / 2; ++q) {
           const int col = col0 + q;
-          z[q] = w * __ldg(p.z0 + state0 + (p.z0_transposed ? col * D + row : row * D + col));
+          z[q] = w * __ldg(p.z0 + state0 + (p.z0_transposed ? row * D + col : col * D + row));
         }
       }
       for (int g = 0; g < seg; ++g) {
@@ -363,8 +380,8 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         }
       }
     }
-    auto publish = [&]() {   // bf16 state for A Z: 64-column blocks of D rows x 128 B
-      if (live) {
+    auto publish = [&]() {   // bf16 Z^T for A Z
+      if (busy) {
 #pragma unroll
         for (int v = 0; v < D / 16; ++v) {
           const int col = col0 + 8 * v;
@@ -378,58 +395,68 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     };
     if constexpr (OUT) publish();
     bool ok = true;
-    // Weights rows [32 part, 32 part + 32) of chunk i into their buffer.
-    auto weight = [&](int i, int part) {
-      const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
-      const int tC = i * C::kPerChunk + kTC, buf = part & 1, use = (i * kParts + part) >> 1;
-      if (part == 0 && !tile_full(tC)) return false;
-      if (use > 0 && !all_ok(mbar_wait(smem_addr(&sm.cs_free[buf]), (use - 1) & 1, ctl))) return false;
-      const uint8_t* src = &sm.tile[tC % NT][part * kPartBlk];
-      const float w = whole ? w_full[part] : w_tail[part];
-      const bool keep = whole || part * kPart + crow < tail;   // other rows may follow in memory
-      const int swz = crow * 128 + ((cvec ^ (crow & 7)) * 16);
-#pragma unroll
-      for (int blk = 0; blk < C::kBlocks; ++blk) {
-        uint4 v = *reinterpret_cast<const uint4*>(src + blk * kBlk + swz);
-        if (!keep) v = make_uint4(0, 0, 0, 0);
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t t[3][4];   // high, middle, low
-        const uint64_t ww = f2_pack(w, w);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint64_t x = f2_mul(bf16x2_to_f2(in[q]), ww);
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            float x0, x1;
-            f2_unpack(x, x0, x1);
-            t[k][q] = pack_bf16x2(x0, x1);
-            if (k + 1 < TERMS) x = f2_sub(x, bf16x2_to_f2(t[k][q]));
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          *reinterpret_cast<uint4*>(&sm.cs[buf][(TERMS - 1 - k) * C::kTerm + blk * kPartBlk + swz]) =
-              make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
-      }
-      fence_async_smem();
-      warp_arrive(sm.cs_ready[buf]);
-      return true;
-    };
-    // The first two parts of a chunk are weighted before the state of the chunk before is
-    // taken, while the tensor core finishes it.
-    ok = n == 0 || (weight(0, 0) && weight(0, 1));
     for (int i = 0; i < n && ok; ++i) {
-      if (!(ok = weight(i, 2) && weight(i, 3))) break;
-      if (i + 1 < n && !(ok = weight(i + 1, 0) && weight(i + 1, 1))) break;
-      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.kv_done), i & 1, ctl)))) break;
+      const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
+      const int tC = i * C::kPerChunk + kTC;
+      if (!(ok = tile_full(tC))) break;
+      // This warp's 32 features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
+      const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
+#pragma unroll 1
+      for (int step = 0; step < C::kSteps; ++step) {
+        const int use = i * C::kSteps + step;
+        if (use > 0 && !(ok = wait(sm.cw_free[grp], use - 1))) break;
+        if (busy) {
+#pragma unroll
+          for (int k = 0; k < C::kStep / 16; ++k) {   // 16 tokens at a time
+            const int tok = grp * kHalf + step * C::kStep + 16 * k;
+            uint32_t r[2][4], t[TERMS][2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int at = tok + 8 * u + (lane & 7);
+              ldmatrix_x4_trans(src + at * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (at & 7)) * 16), r[u]);
+              const int pair = (tok + 8 * u) / 2 + (lane & 3);   // this lane's two tokens
+              const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
+              if (!whole) {   // rows past the chunk's tokens may hold anything
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                  r[u][m] = 2 * pair + 1 < tail ? r[u][m] : 2 * pair < tail ? r[u][m] & 0xffffu : 0u;
+              }
+              const uint64_t ww = f2_pack(w.x, w.y);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                uint64_t x = f2_mul(bf16x2_to_f2(r[u][m]), ww);
+#pragma unroll
+                for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
+                  float x0, x1;
+                  f2_unpack(x, x0, x1);
+                  t[e][u][m] = pack_bf16x2(x0, x1);
+                  if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][u][m]));
+                }
+              }
+            }
+            const uint32_t dst = tCw + lane_off + grp * C::kGroupCols + 8 * k;
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) {
+              const uint32_t col = dst + e * (C::kStep / 2);
+              tmem_st_16x128b_x2(col, t[e][0][0], t[e][0][1], t[e][1][0], t[e][1][1]);
+              tmem_st_16x128b_x2(col + (16u << 16), t[e][0][2], t[e][0][3], t[e][1][2], t[e][1][3]);
+            }
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        warp_arrive(sm.cw_ready[grp]);
+      }
+      if (!ok) break;
+      if (!(ok = wait(sm.kv_done, i))) break;
       tc_fence_after();
-      const double dl = chunk_at<REV>(p, ci0 + i).len == kChunk ? d_full : d_tail;
+      const double dl = whole ? d_full : d_tail;
       const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
-      if (quad * 32 < D) {
+      if (busy) {
 #pragma unroll
         for (int q = 0; q < D / 2; q += 32) {
           uint32_t t0[32];
-          tmem_ld32(tKV + q, t0);
+          tmem_ld32(tbase + lane_off + col0 + q, t0);
 #pragma unroll
           for (int k = 0; k < 32; ++k) z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, __uint_as_float(t0[k])));
         }
@@ -438,18 +465,22 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       if (i + 1 < n) {
         warp_arrive(sm.kv_free);
         if constexpr (OUT) {
-          if (!(ok = all_ok(mbar_wait(smem_addr(&sm.qz_done), i & 1, ctl)))) break;
+          if (!(ok = wait(sm.az_done, i))) break;
           publish();
         }
       }
     }
-    if (ok && live && (!OUT || (seg == p.nseg - 1 && p.z_out != nullptr))) {
-      float4* dst = reinterpret_cast<float4*>(
-          OUT ? p.z_out + state0 + row * D + col0
-              : p.zseg + (static_cast<int64_t>(bh) * (p.nseg - 1) + seg) * (D * D)) + (OUT ? 0 : zt);
+    if (ok && busy) {
+      if (!OUT) {
+        float4* dst = reinterpret_cast<float4*>(
+                          p.zseg + (static_cast<int64_t>(bh) * (p.nseg - 1) + seg) * (D * D)) + zt;
 #pragma unroll
-      for (int q = 0; q < D / 8; ++q)
-        dst[q * (OUT ? 1 : 2 * D)] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+        for (int q = 0; q < D / 8; ++q)
+          dst[q * (2 * D)] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+      } else if (seg == p.nseg - 1 && p.z_out != nullptr) {
+#pragma unroll
+        for (int q = 0; q < D / 2; ++q) p.z_out[state0 + static_cast<int64_t>(col0 + q) * D + row] = z[q];
+      }
     }
   } else if (OUT && warp < 12) {
     // --------------------------------- masked scores and output, one row per lane
@@ -471,7 +502,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const ChunkAt c = chunk_at<REV>(p, ci0 + i);
-      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.s_full), i & 1, ctl)))) break;
+      if (!(ok = wait(sm.s_full, i))) break;
       tc_fence_after();
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -508,52 +539,57 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         }
         tmem_st16(tS + lane_off + 16 * m, pk);
       }
+      // A Z, scaled in place by the decay since the chunk's start.
+      const int x = REV ? c.len - 1 - row : row + 1;
+      const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
+      if (!(ok = wait(sm.az_done, i))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < D; q += 32) {
+        uint32_t az[32];
+        tmem_ld32(tY + lane_off + q, az);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) az[k] = __float_as_uint(__uint_as_float(az[k]) * w);
+        tmem_st16(tY + lane_off + q, az);
+        tmem_st16(tY + lane_off + q + 16, az + 16);
+      }
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(sm.p_ready);
-      const int x = REV ? c.len - 1 - row : row + 1;
-      const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
-      const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
-      __nv_bfloat16* dst = p.y + (tok * p.H + h) * D;
-      if (!(ok = all_ok(mbar_wait(smem_addr(&sm.y_full), i & 1, ctl)))) break;
+      if (!(ok = wait(sm.y_full, i))) break;
       tc_fence_after();
-      // Through shared memory and a TMA store, 64 columns at a time; a warp whose rows
-      // end inside the chunk stores them itself (the rows after may be another rank's).
-      const bool staged = quad * 32 + 32 <= c.len;
+      uint32_t out[D / 2];
 #pragma unroll
-      for (int half = 0; half < C::kBlocks; ++half) {
-        uint32_t out[32];
+      for (int q = 0; q < D; q += 32) {
+        uint32_t y[32];
+        tmem_ld32(tY + lane_off + q, y);
 #pragma unroll
-        for (int q = 0; q < 64; q += 16) {
-          uint32_t az[16], pc[16];
-          tmem_ld16(tAZ + lane_off + half * 64 + q, az);
-          tmem_ld16(tPC + lane_off + half * 64 + q, pc);
+        for (int k = 0; k < 16; ++k)
+          out[q / 2 + k] = pack_bf16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+      }
+      tc_fence_before();
+      warp_arrive(sm.y_free);
+      // Through shared memory and TMA stores of 32 rows x 64 columns (a thread's own stores
+      // would touch 32 lines at a time and hold up the other warps' shared-memory accesses); a
+      // warp whose rows end inside the chunk stores them itself, the rows after may be another
+      // piece's.
+      if (quad * 32 + 32 <= c.len) {
+        if (lane == 0) bulk_wait_read<0>();   // the chunk before has left the buffers
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            out[q / 2 + k] = pack_bf16x2(fmaf(__uint_as_float(az[2 * k]), w, __uint_as_float(pc[2 * k])),
-                                         fmaf(__uint_as_float(az[2 * k + 1]), w, __uint_as_float(pc[2 * k + 1])));
-        }
-        if (half + 1 == C::kBlocks) {
-          tc_fence_before();
-          warp_arrive(sm.y_free);
-        }
-        if (staged) {
-          if (lane == 0) bulk_wait_read();   // the store before has left the buffer
-          __syncwarp();
+        for (int k = 0; k < D / 8; ++k)
+          *reinterpret_cast<uint4*>(&sm.y[k / 8][quad][lane * 128 + (((k % 8) ^ (lane & 7)) * 16)]) =
+              make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int blk = 0; blk < C::kBlocks; ++blk)
+            tma_store_4d(&tm_y, smem_addr(&sm.y[blk][quad][0]), blk * 64, h, c.t0 + quad * 32, c.rank * p.B + b);
+      } else if (row < c.len) {
+        const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
+        uint4* dst = reinterpret_cast<uint4*>(p.y + (tok * p.H + h) * D);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(&sm.y[quad][lane * 128 + ((k ^ (lane & 7)) * 16)]) =
-                make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0)
-            tma_store_4d(&tm_y, smem_addr(&sm.y[quad][0]), half * 64, h, c.t0 + quad * 32, c.rank * p.B + b);
-        } else if (row < c.len) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<uint4*>(dst + half * 64)[k] =
-                make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-        }
+        for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
       }
     }
     if (lane == 0) bulk_wait_all();
