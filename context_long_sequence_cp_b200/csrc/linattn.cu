@@ -61,16 +61,18 @@ struct LinCfg {
   static constexpr int kTiles = D == 128 ? (OUT ? 5 : 6) : (OUT ? 9 : 10);
   static constexpr int kThreads = OUT ? 448 : 320;
   static constexpr int kMmaWarp = OUT ? 12 : 8;
-  // Tokens a group weights at a time, so that the terms of both groups fit 128 columns.
-  static constexpr int kStep = TERMS == 3 ? 32 : 64;
+  // Tokens a group of four warps weights at a time, and the buffers it alternates between.
+  static constexpr int kStep = OUT ? 16 : 32;
+  static constexpr int kBufs = OUT && TERMS == 3 ? 1 : 2;
   static constexpr int kSteps = kHalf / kStep;
-  // TMEM columns: chunk state, transposed [0,128); weighted C^T [128,256), a group's
-  // terms side by side in bf16 pairs; with OUT the scores/P [256,384) and the output
+  // TMEM columns: chunk state, transposed [0,128); weighted C^T from 128 on, a buffer's
+  // terms side by side in bf16 pairs; with OUT: P [192,256), scores [256,384), output
   // [384,512).
-  static constexpr int kTmemCols = OUT ? 512 : 256;
-  static constexpr int kGroupCols = TERMS * kStep / 2;
+  static constexpr int kBufCols = TERMS * kStep / 2;
+  static constexpr int kTmemCols = 512;
+  static_assert(!OUT || 2 * kBufs * kBufCols <= 64, "weighted C^T columns");
 };
-constexpr int kColCw = 128, kColS = 256, kColY = 384;
+constexpr int kColCw = 128, kColP = 192, kColS = 256, kColY = 384;
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // A B^T
 // A Z: both operands K-major. C^T B and P C: left operand in TMEM, right MN-major.
 __host__ __device__ constexpr uint32_t idesc_az(int D) { return idesc_bf16_f32(128, D, 0, 0); }
@@ -83,9 +85,10 @@ struct alignas(1024) LinSmem {
   uint8_t z[OUT ? D * D * 2 : 1024];                 // bf16 Z^T: row = feature of C, 64-column blocks
   uint8_t y[OUT ? D / 64 : 1][OUT ? 4 : 1][OUT ? 32 * 128 : 1024];   // output: 32 rows x 64 columns per warp
   uint64_t full[C::kTiles], empty[C::kTiles];
-  uint64_t cw_ready[2], cw_free[2];                  // per group of weighting warps
-  uint64_t s_full, p_ready, kv_done, kv_free, az_done, z_ready, y_full, y_free, drain;
-  alignas(16) float pow32[64];                       // [32 + x] = d^x for x = 0 .. 31, 0 below
+  uint64_t cw_ready[2][2], cw_free[2][2];            // per group of weighting warps and buffer
+  uint64_t s_full, s_free, p_ready, kv_done, kv_free, az_done, z_ready, y_full, y_free, drain;
+  alignas(16) float pow32[32];                       // d^0 .. d^31
+  float diag[64];                                    // [32 + x] = s_in d^x for x = 0 .. 31, 0 below
   float2 w_full[kChunk / 2], w_tail[kChunk / 2];     // weights of the rows of C, of a whole and of a tail chunk
   uint32_t tmem_base;
   WaitBlock wblk;
@@ -200,11 +203,12 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       mbar_init(smem_addr(&sm.full[s]), 1);
       mbar_init(smem_addr(&sm.empty[s]), 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_addr(&sm.cw_ready[s]), 4);
-      mbar_init(smem_addr(&sm.cw_free[s]), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(smem_addr(&sm.cw_ready[s >> 1][s & 1]), 4);
+      mbar_init(smem_addr(&sm.cw_free[s >> 1][s & 1]), 1);
     }
     mbar_init(smem_addr(&sm.s_full), 1);
+    mbar_init(smem_addr(&sm.s_free), 4);
     mbar_init(smem_addr(&sm.p_ready), 4);
     mbar_init(smem_addr(&sm.kv_done), 1);
     mbar_init(smem_addr(&sm.kv_free), 8);
@@ -216,8 +220,12 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     wait_block_init(sm.wblk, p.status, p.wait_limit_ns);
     fence_barrier_init();
   }
-  if (threadIdx.x < 64)
-    sm.pow32[threadIdx.x] = threadIdx.x < 32 ? 0.f : static_cast<float>(decay_pow(ld, threadIdx.x - 32));
+  if (threadIdx.x < 32) {
+    const float w = static_cast<float>(decay_pow(ld, threadIdx.x));
+    sm.pow32[threadIdx.x] = w;
+    sm.diag[threadIdx.x] = 0.f;
+    sm.diag[32 + threadIdx.x] = w * p.s_in;
+  }
   if (threadIdx.x < 256) {
     const int r = threadIdx.x & 127, len = threadIdx.x < 128 ? kChunk : tail;
     const float w = r < len ? static_cast<float>(decay_pow(ld, REV ? r + 1 : len - 1 - r)) * p.s_upd : 0.f;
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl ctl = wait_ctl(sm.wblk);
-  const uint32_t tCw = tbase + kColCw, tS = tbase + kColS, tY = tbase + kColY;
+  const uint32_t tCw = tbase + kColCw, tP = tbase + kColP, tS = tbase + kColS, tY = tbase + kColY;
   auto wait = [&](uint64_t& bar, int phase) { return all_ok(mbar_wait(smem_addr(&bar), phase & 1, ctl)); };
   auto tile_full = [&](int t) { return wait(sm.full[t % NT], t / NT); };
 
@@ -278,26 +286,31 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     constexpr uint32_t kIdescAZ = idesc_az(D), kIdescTS = idesc_ts(D);
     const uint64_t dZ = smem_desc_sw128(smem_addr(&sm.z[0]), 16, 1024);
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
+    auto tile_addr = [&](int t) { return smem_addr(&sm.tile[t % NT][0]); };
+    auto scores = [&](int i) {   // S of chunk i, once its predecessor's has been read
+      const int tA = i * C::kPerChunk + kTA, tB = i * C::kPerChunk + kTB;
+      if (!tile_full(tA) || !tile_full(tB)) return false;
+      if (i > 0 && !wait(sm.s_free, i - 1)) return false;
+      tc_fence_after();
+      const uint64_t dA = smem_desc_sw128(tile_addr(tA), 16, 1024), dB = smem_desc_sw128(tile_addr(tB), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
+        umma_ss_elect(tS, desc_at(dA, off), desc_at(dB, off), kIdescS, kk > 0);
+      }
+      umma_commit_elect(smem_addr(&sm.s_full));
+      return true;
+    };
+    if constexpr (OUT) ok = n == 0 || scores(0);
+    for (int i = 0; i < n && ok; ++i) {
       const int tA = i * C::kPerChunk + kTA, tB = i * C::kPerChunk + kTB, tC = i * C::kPerChunk + kTC;
-      const uint32_t aA = smem_addr(&sm.tile[tA % NT][0]), aB = smem_addr(&sm.tile[tB % NT][0]),
-                     aC = smem_addr(&sm.tile[tC % NT][0]);
       if (!(ok = tile_full(tB))) break;
       if constexpr (OUT) {
-        if (!(ok = tile_full(tA))) break;
-        tc_fence_after();
-        // Scores. P of the previous chunk shares the columns: its product was issued before.
-        const uint64_t dA = smem_desc_sw128(aA, 16, 1024), dB = smem_desc_sw128(aB, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
-          umma_ss_elect(tS, desc_at(dA, off), desc_at(dB, off), kIdescS, kk > 0);
-        }
-        umma_commit_elect(smem_addr(&sm.s_full));
         // A Z, onto the columns the output warps have read for the previous chunk.
         if (!(ok = wait(sm.z_ready, i))) break;
         if (i > 0 && !(ok = wait(sm.y_free, i - 1))) break;
         tc_fence_after();
+        const uint64_t dA = smem_desc_sw128(tile_addr(tA), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_ss_elect(tY, desc_at(dA, (kk >> 2) * kBlk + (kk & 3) * 32),
@@ -307,31 +320,32 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       }
       // Chunk state, as the weighted rows of C come, smallest term first.
       if (i > 0 && !(ok = wait(sm.kv_free, i - 1))) break;
-      const uint64_t dBn = smem_desc_sw128(aB, kBlk, 1024);
+      const uint64_t dBn = smem_desc_sw128(tile_addr(tB), kBlk, 1024);
       for (int part = 0; part < 2 * C::kSteps; ++part) {
-        const int g = part & 1, step = part >> 1;
-        if (!(ok = wait(sm.cw_ready[g], i * C::kSteps + step))) break;
+        const int g = part & 1, step = part >> 1, u = i * C::kSteps + step, buf = u % C::kBufs;
+        if (!(ok = wait(sm.cw_ready[g][buf], u / C::kBufs))) break;
         tc_fence_after();
         const uint64_t d = desc_at(dBn, (g * kHalf + step * C::kStep) * 128);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
           for (int kk = 0; kk < C::kStep / 16; ++kk)
-            umma_ts_elect(tbase, tCw + g * C::kGroupCols + term * (C::kStep / 2) + kk * 8, desc_at(d, kk * 2048),
-                          kIdescTS, part > 0 || term > 0 || kk > 0);
-        umma_commit_elect(smem_addr(&sm.cw_free[g]));
+            umma_ts_elect(tbase, tCw + (g * C::kBufs + buf) * C::kBufCols + term * (C::kStep / 2) + kk * 8,
+                          desc_at(d, kk * 2048), kIdescTS, part > 0 || term > 0 || kk > 0);
+        umma_commit_elect(smem_addr(&sm.cw_free[g][buf]));
       }
       if (!ok) break;
       umma_commit_elect(smem_addr(&sm.kv_done));
       umma_commit_elect(smem_addr(&sm.empty[tB % NT]));
       if constexpr (OUT) {
+        if (i + 1 < n && !(ok = scores(i + 1))) break;
         if (!(ok = tile_full(tC))) break;
         if (!(ok = wait(sm.p_ready, i))) break;   // P written, and A Z scaled: P C adds to it
         tc_fence_after();
-        const uint64_t dC = smem_desc_sw128(aC, kBlk, 1024);
+        const uint64_t dC = smem_desc_sw128(tile_addr(tC), kBlk, 1024);
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
-          umma_ts_elect(tY, tS + kk * 8, desc_at(dC, kk * 2048), kIdescTS, 1u);
+          umma_ts_elect(tY, tP + kk * 8, desc_at(dC, kk * 2048), kIdescTS, 1u);
         umma_commit_elect(smem_addr(&sm.y_full));
       }
       umma_commit_elect(smem_addr(&sm.empty[tC % NT]));
@@ -395,62 +409,67 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     };
     if constexpr (OUT) publish();
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
-      const int tC = i * C::kPerChunk + kTC;
-      if (!(ok = tile_full(tC))) break;
-      // This warp's 32 features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
-      const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
-#pragma unroll 1
-      for (int step = 0; step < C::kSteps; ++step) {
-        const int use = i * C::kSteps + step;
-        if (use > 0 && !(ok = wait(sm.cw_free[grp], use - 1))) break;
-        if (busy) {
+    // Weights this warp's 32 features of one step's tokens into a TMEM buffer.
+    auto weight = [&](int i, int step) {
+      const int tC = i * C::kPerChunk + kTC, u = i * C::kSteps + step, buf = u % C::kBufs;
+      if (step == 0 && !tile_full(tC)) return false;
+      if (u >= C::kBufs && !wait(sm.cw_free[grp][buf], u / C::kBufs - 1)) return false;
+      if (busy) {
+        const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
+        // The features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
+        const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
 #pragma unroll
-          for (int k = 0; k < C::kStep / 16; ++k) {   // 16 tokens at a time
-            const int tok = grp * kHalf + step * C::kStep + 16 * k;
-            uint32_t r[2][4], t[TERMS][2][4];
+        for (int k = 0; k < C::kStep / 16; ++k) {   // 16 tokens at a time
+          const int tok = grp * kHalf + step * C::kStep + 16 * k;
+          uint32_t r[2][4], t[TERMS][2][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int at = tok + 8 * u + (lane & 7);
-              ldmatrix_x4_trans(src + at * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (at & 7)) * 16), r[u]);
-              const int pair = (tok + 8 * u) / 2 + (lane & 3);   // this lane's two tokens
-              const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
-              if (!whole) {   // rows past the chunk's tokens may hold anything
+          for (int v = 0; v < 2; ++v) {
+            const int at = tok + 8 * v + (lane & 7);
+            ldmatrix_x4_trans(src + at * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) * 16), r[v]);
+            const int pair = (tok + 8 * v) / 2 + (lane & 3);   // this lane's two tokens
+            const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
+            if (!whole) {   // rows past the chunk's tokens may hold anything
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                  r[u][m] = 2 * pair + 1 < tail ? r[u][m] : 2 * pair < tail ? r[u][m] & 0xffffu : 0u;
-              }
-              const uint64_t ww = f2_pack(w.x, w.y);
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                uint64_t x = f2_mul(bf16x2_to_f2(r[u][m]), ww);
-#pragma unroll
-                for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
-                  float x0, x1;
-                  f2_unpack(x, x0, x1);
-                  t[e][u][m] = pack_bf16x2(x0, x1);
-                  if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][u][m]));
-                }
-              }
+              for (int m = 0; m < 4; ++m)
+                r[v][m] = 2 * pair + 1 < tail ? r[v][m] : 2 * pair < tail ? r[v][m] & 0xffffu : 0u;
             }
-            const uint32_t dst = tCw + lane_off + grp * C::kGroupCols + 8 * k;
+            const uint64_t ww = f2_pack(w.x, w.y);
 #pragma unroll
-            for (int e = 0; e < TERMS; ++e) {
-              const uint32_t col = dst + e * (C::kStep / 2);
-              tmem_st_16x128b_x2(col, t[e][0][0], t[e][0][1], t[e][1][0], t[e][1][1]);
-              tmem_st_16x128b_x2(col + (16u << 16), t[e][0][2], t[e][0][3], t[e][1][2], t[e][1][3]);
+            for (int m = 0; m < 4; ++m) {
+              uint64_t x = f2_mul(bf16x2_to_f2(r[v][m]), ww);
+#pragma unroll
+              for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
+                float x0, x1;
+                f2_unpack(x, x0, x1);
+                t[e][v][m] = pack_bf16x2(x0, x1);
+                if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][v][m]));
+              }
             }
           }
-          tmem_st_wait();
+          const uint32_t dst = tCw + lane_off + (grp * C::kBufs + buf) * C::kBufCols + 8 * k;
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e) {
+            const uint32_t col = dst + e * (C::kStep / 2);
+            tmem_st_16x128b_x2(col, t[e][0][0], t[e][0][1], t[e][1][0], t[e][1][1]);
+            tmem_st_16x128b_x2(col + (16u << 16), t[e][0][2], t[e][0][3], t[e][1][2], t[e][1][3]);
+          }
         }
-        tc_fence_before();
-        warp_arrive(sm.cw_ready[grp]);
+        tmem_st_wait();
       }
-      if (!ok) break;
-      if (!(ok = wait(sm.kv_done, i))) break;
+      tc_fence_before();
+      warp_arrive(sm.cw_ready[grp][buf]);
+      return true;
+    };
+    // With two buffers a chunk's first step is weighted before the state of the chunk before
+    // is taken, while the tensor core finishes that.
+    constexpr int kAhead = C::kBufs - 1;
+    for (int step = 0; step < kAhead && n > 0 && ok; ++step) ok = weight(0, step);
+    for (int i = 0; i < n && ok; ++i) {
+      for (int step = kAhead; step < C::kSteps && ok; ++step) ok = weight(i, step);
+      for (int step = 0; step < kAhead && i + 1 < n && ok; ++step) ok = weight(i + 1, step);
+      if (!ok || !(ok = wait(sm.kv_done, i))) break;
       tc_fence_after();
-      const double dl = whole ? d_full : d_tail;
+      const double dl = chunk_at<REV>(p, ci0 + i).len == kChunk ? d_full : d_tail;
       const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
       if (busy) {
 #pragma unroll
@@ -497,8 +516,14 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       const int x = REV ? 32 * m - row : row - 32 * m - 31;
       f[m] = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_in : p.s_in;
     }
-    const float4* off = reinterpret_cast<const float4*>(&sm.pow32[32]);
-    const float* diag = &sm.pow32[32 + (REV ? -lane : lane)];   // column jj at REV ? +jj : -jj
+    const float4* off = reinterpret_cast<const float4*>(&sm.pow32[0]);
+    const float* diag = &sm.diag[32 + (REV ? -lane : lane)];   // column jj at REV ? +jj : -jj
+    // The masked blocks of P are zero for good.
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint32_t zero[16] = {0u};
+      if (REV ? m < quad : m > quad) tmem_st16(tP + lane_off + 16 * m, zero);
+    }
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const ChunkAt c = chunk_at<REV>(p, ci0 + i);
@@ -506,39 +531,35 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        uint32_t pk[16];
-        if (REV ? m < quad : m > quad) {
+        if (REV ? m < quad : m > quad) continue;
+        uint32_t s[32], pk[16];
+        tmem_ld32(tS + lane_off + 32 * m, s);
+        if (REV && c.len < kChunk) {   // columns past the chunk's tokens hold other rows
 #pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = 0u;
-        } else {
-          uint32_t s[32];
-          tmem_ld32(tS + lane_off + 32 * m, s);
-          if (REV && c.len < kChunk) {   // columns past the chunk's tokens hold other rows
-#pragma unroll
-            for (int jj = 0; jj < 32; ++jj) s[jj] = 32 * m + jj < c.len ? s[jj] : 0u;
-          }
-          if (m == quad) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int j0 = 2 * j, j1 = 2 * j + 1;
-              const float w0 = diag[REV ? j0 : -j0] * p.s_in, w1 = diag[REV ? j1 : -j1] * p.s_in;
-              const bool k0 = REV ? j0 >= lane : j0 <= lane, k1 = REV ? j1 >= lane : j1 <= lane;
-              pk[j] = pack_bf16x2(k0 ? __uint_as_float(s[j0]) * w0 : 0.f, k1 ? __uint_as_float(s[j1]) * w1 : 0.f);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 v = off[REV ? q : 7 - q];
-              const float w[4] = {REV ? v.x : v.w, REV ? v.y : v.z, REV ? v.z : v.y, REV ? v.w : v.x};
-              pk[2 * q] = pack_bf16x2(__uint_as_float(s[4 * q]) * (f[m] * w[0]),
-                                      __uint_as_float(s[4 * q + 1]) * (f[m] * w[1]));
-              pk[2 * q + 1] = pack_bf16x2(__uint_as_float(s[4 * q + 2]) * (f[m] * w[2]),
-                                          __uint_as_float(s[4 * q + 3]) * (f[m] * w[3]));
-            }
-          }
+          for (int jj = 0; jj < 32; ++jj) s[jj] = 32 * m + jj < c.len ? s[jj] : 0u;
         }
-        tmem_st16(tS + lane_off + 16 * m, pk);
+        const uint64_t ff = f2_pack(f[m], f[m]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint64_t w0, w1;
+          if (m == quad) {
+            w0 = f2_pack(diag[REV ? 4 * q : -4 * q], diag[REV ? 4 * q + 1 : -4 * q - 1]);
+            w1 = f2_pack(diag[REV ? 4 * q + 2 : -4 * q - 2], diag[REV ? 4 * q + 3 : -4 * q - 3]);
+          } else {
+            const float4 v = off[REV ? q : 7 - q];
+            w0 = f2_mul(REV ? f2_pack(v.x, v.y) : f2_pack(v.w, v.z), ff);
+            w1 = f2_mul(REV ? f2_pack(v.z, v.w) : f2_pack(v.y, v.x), ff);
+          }
+          float x0, x1;
+          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), w0), x0, x1);
+          pk[2 * q] = pack_bf16x2(x0, x1);
+          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), w1), x0, x1);
+          pk[2 * q + 1] = pack_bf16x2(x0, x1);
+        }
+        tmem_st16(tP + lane_off + 16 * m, pk);
       }
+      tc_fence_before();
+      warp_arrive(sm.s_free);   // the next chunk's scores may come
       // A Z, scaled in place by the decay since the chunk's start.
       const int x = REV ? c.len - 1 - row : row + 1;
       const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
