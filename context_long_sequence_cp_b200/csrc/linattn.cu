@@ -59,20 +59,23 @@ struct LinCfg {
   static constexpr int kTileBytes = kBlocks * kBlk;       // a 128 x D tile
   static constexpr int kPerChunk = OUT ? 3 : 2;           // tiles per chunk: [A,] B, C
   static constexpr int kTiles = D == 128 ? (OUT ? 5 : 6) : (OUT ? 9 : 10);
-  static constexpr int kThreads = OUT ? 448 : 320;
-  static constexpr int kMmaWarp = OUT ? 12 : 8;
+  // Warps 0-7 weight C and hold the state; 8-11 (OUT) scores and output; then the issuers: the
+  // chunk state's products, the TMA, and (OUT) the other products. Two issuing warps, because
+  // one spends longer on its waits and commits than the tensor core on the products.
+  static constexpr int kKvWarp = OUT ? 12 : 8, kTmaWarp = kKvWarp + 1, kOutWarp = kKvWarp + 2;
+  static constexpr int kThreads = 32 * (OUT ? kOutWarp + 1 : kOutWarp);
   // Tokens a group of four warps weights at a time, and the buffers it alternates between.
-  static constexpr int kStep = OUT ? 16 : 32;
-  static constexpr int kBufs = OUT && TERMS == 3 ? 1 : 2;
+  static constexpr int kStep = OUT && TERMS == 3 ? 32 : 64;
+  static constexpr int kBufs = OUT ? 1 : 2;
   static constexpr int kSteps = kHalf / kStep;
   // TMEM columns: chunk state, transposed [0,128); weighted C^T from 128 on, a buffer's
-  // terms side by side in bf16 pairs; with OUT: P [192,256), scores [256,384), output
-  // [384,512).
+  // terms side by side in bf16 pairs; with OUT: scores, P over their lower half [256,384),
+  // output [384,512).
   static constexpr int kBufCols = TERMS * kStep / 2;
   static constexpr int kTmemCols = 512;
-  static_assert(!OUT || 2 * kBufs * kBufCols <= 64, "weighted C^T columns");
+  static_assert(2 * kBufs * kBufCols <= (OUT ? 128 : 384), "weighted C^T columns");
 };
-constexpr int kColCw = 128, kColP = 192, kColS = 256, kColY = 384;
+constexpr int kColCw = 128, kColS = 256, kColY = 384;
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // A B^T
 // A Z: both operands K-major. C^T B and P C: left operand in TMEM, right MN-major.
 __host__ __device__ constexpr uint32_t idesc_az(int D) { return idesc_bf16_f32(128, D, 0, 0); }
@@ -86,9 +89,8 @@ struct alignas(1024) LinSmem {
   uint8_t y[OUT ? D / 64 : 1][OUT ? 4 : 1][OUT ? 32 * 128 : 1024];   // output: 32 rows x 64 columns per warp
   uint64_t full[C::kTiles], empty[C::kTiles];
   uint64_t cw_ready[2][2], cw_free[2][2];            // per group of weighting warps and buffer
-  uint64_t s_full, s_free, p_ready, kv_done, kv_free, az_done, z_ready, y_full, y_free, drain;
-  alignas(16) float pow32[32];                       // d^0 .. d^31
-  float diag[64];                                    // [32 + x] = s_in d^x for x = 0 .. 31, 0 below
+  uint64_t s_full, p_ready, kv_done, kv_free, az_done, z_ready, y_full, y_free, drain[2];
+  float diag[64];                                    // fast decays: [32 + x] = s_in d^x for x = 0 .. 31
   float2 w_full[kChunk / 2], w_tail[kChunk / 2];     // weights of the rows of C, of a whole and of a tail chunk
   uint32_t tmem_base;
   WaitBlock wblk;
@@ -97,6 +99,9 @@ static_assert(sizeof(LinSmem<128, true, 2>) + 1024 <= 232448, "LinSmem exceeds t
 static_assert(sizeof(LinSmem<64, true, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
 static_assert(sizeof(LinSmem<128, false, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
 static_assert(sizeof(LinSmem<64, false, 2>) + 1024 <= 232448, "LinSmem exceeds the per-CTA limit");
+
+// Decays slow enough that d^-128 stays below e^48: see the score warps.
+constexpr double kSlowDecay = -48.0 / kChunk;
 
 // Descriptor moved by a byte offset (the address field counts 16-byte units).
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
@@ -172,6 +177,10 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&bar));
 }
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <int D, bool OUT, bool REV, int TERMS>
@@ -201,14 +210,13 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NT; ++s) {
       mbar_init(smem_addr(&sm.full[s]), 1);
-      mbar_init(smem_addr(&sm.empty[s]), 1);
+      mbar_init(smem_addr(&sm.empty[s]), OUT ? 2 : 1);   // a commit of each reader of the tile
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(smem_addr(&sm.cw_ready[s >> 1][s & 1]), 4);
       mbar_init(smem_addr(&sm.cw_free[s >> 1][s & 1]), 1);
     }
     mbar_init(smem_addr(&sm.s_full), 1);
-    mbar_init(smem_addr(&sm.s_free), 4);
     mbar_init(smem_addr(&sm.p_ready), 4);
     mbar_init(smem_addr(&sm.kv_done), 1);
     mbar_init(smem_addr(&sm.kv_free), 8);
@@ -216,26 +224,24 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     mbar_init(smem_addr(&sm.z_ready), 8);
     mbar_init(smem_addr(&sm.y_full), 1);
     mbar_init(smem_addr(&sm.y_free), 4);
-    mbar_init(smem_addr(&sm.drain), 1);
+    mbar_init(smem_addr(&sm.drain[0]), 1);
+    mbar_init(smem_addr(&sm.drain[1]), 1);
     wait_block_init(sm.wblk, p.status, p.wait_limit_ns);
     fence_barrier_init();
   }
-  if (threadIdx.x < 32) {
-    const float w = static_cast<float>(decay_pow(ld, threadIdx.x));
-    sm.pow32[threadIdx.x] = w;
-    sm.diag[threadIdx.x] = 0.f;
-    sm.diag[32 + threadIdx.x] = w * p.s_in;
-  }
+  const bool slow = ld >= kSlowDecay;
+  if (OUT && threadIdx.x < 64)
+    sm.diag[threadIdx.x] = threadIdx.x < 32 ? 0.f : static_cast<float>(decay_pow(ld, threadIdx.x - 32)) * p.s_in;
   if (threadIdx.x < 256) {
     const int r = threadIdx.x & 127, len = threadIdx.x < 128 ? kChunk : tail;
     const float w = r < len ? static_cast<float>(decay_pow(ld, REV ? r + 1 : len - 1 - r)) * p.s_upd : 0.f;
     reinterpret_cast<float*>(threadIdx.x < 128 ? sm.w_full : sm.w_tail)[r] = w;
   }
-  if (warp == C::kMmaWarp) {
+  if (warp == C::kKvWarp) {
     tmem_alloc(smem_addr(&sm.tmem_base), C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == C::kMmaWarp + 1 && lane == 0) {
+  if (warp == C::kTmaWarp && lane == 0) {
     prefetch_tensormap(&tm_a);
     prefetch_tensormap(&tm_b);
     prefetch_tensormap(&tm_c);
@@ -245,11 +251,11 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl ctl = wait_ctl(sm.wblk);
-  const uint32_t tCw = tbase + kColCw, tP = tbase + kColP, tS = tbase + kColS, tY = tbase + kColY;
+  const uint32_t tCw = tbase + kColCw, tS = tbase + kColS, tY = tbase + kColY;
   auto wait = [&](uint64_t& bar, int phase) { return all_ok(mbar_wait(smem_addr(&bar), phase & 1, ctl)); };
   auto tile_full = [&](int t) { return wait(sm.full[t % NT], t / NT); };
 
-  if (warp == C::kMmaWarp + 1) {
+  if (warp == C::kTmaWarp) {
     // ---------------------------------------------------------------- TMA
     const uint64_t pol = l2_policy_evict_first();
     bool ok = true;
@@ -281,51 +287,23 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     if (!ok)   // abort: let every load this warp issued land before the CTA exits
       for (int k = t - NT; k < t; ++k)
         if (k >= 0) mbar_wait_drain(smem_addr(&sm.full[k % NT]), (k / NT) & 1, p.wait_limit_ns);
-  } else if (warp == C::kMmaWarp) {
-    // ---------------------------------------------------------------- MMA
-    constexpr uint32_t kIdescAZ = idesc_az(D), kIdescTS = idesc_ts(D);
-    const uint64_t dZ = smem_desc_sw128(smem_addr(&sm.z[0]), 16, 1024);
+  } else if (warp == C::kKvWarp) {
+    // ---------------------------------------- MMA: C^T B of a chunk, onto the chunk state
+    constexpr uint32_t kIdescTS = idesc_ts(D);
     bool ok = true;
-    auto tile_addr = [&](int t) { return smem_addr(&sm.tile[t % NT][0]); };
-    auto scores = [&](int i) {   // S of chunk i, once its predecessor's has been read
-      const int tA = i * C::kPerChunk + kTA, tB = i * C::kPerChunk + kTB;
-      if (!tile_full(tA) || !tile_full(tB)) return false;
-      if (i > 0 && !wait(sm.s_free, i - 1)) return false;
-      tc_fence_after();
-      const uint64_t dA = smem_desc_sw128(tile_addr(tA), 16, 1024), dB = smem_desc_sw128(tile_addr(tB), 16, 1024);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
-        umma_ss_elect(tS, desc_at(dA, off), desc_at(dB, off), kIdescS, kk > 0);
-      }
-      umma_commit_elect(smem_addr(&sm.s_full));
-      return true;
-    };
-    if constexpr (OUT) ok = n == 0 || scores(0);
+#pragma unroll 1
     for (int i = 0; i < n && ok; ++i) {
-      const int tA = i * C::kPerChunk + kTA, tB = i * C::kPerChunk + kTB, tC = i * C::kPerChunk + kTC;
+      const int tB = i * C::kPerChunk + kTB, tC = i * C::kPerChunk + kTC;
       if (!(ok = tile_full(tB))) break;
-      if constexpr (OUT) {
-        // A Z, onto the columns the output warps have read for the previous chunk.
-        if (!(ok = wait(sm.z_ready, i))) break;
-        if (i > 0 && !(ok = wait(sm.y_free, i - 1))) break;
-        tc_fence_after();
-        const uint64_t dA = smem_desc_sw128(tile_addr(tA), 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_elect(tY, desc_at(dA, (kk >> 2) * kBlk + (kk & 3) * 32),
-                        desc_at(dZ, (kk >> 2) * (D * 128) + (kk & 3) * 32), kIdescAZ, kk > 0);
-        umma_commit_elect(smem_addr(&sm.az_done));
-        umma_commit_elect(smem_addr(&sm.empty[tA % NT]));
-      }
-      // Chunk state, as the weighted rows of C come, smallest term first.
       if (i > 0 && !(ok = wait(sm.kv_free, i - 1))) break;
-      const uint64_t dBn = smem_desc_sw128(tile_addr(tB), kBlk, 1024);
+      const uint64_t dB = smem_desc_sw128(smem_addr(&sm.tile[tB % NT][0]), kBlk, 1024);
+      // As the weighted rows of C come, smallest term first.
+#pragma unroll 1
       for (int part = 0; part < 2 * C::kSteps; ++part) {
         const int g = part & 1, step = part >> 1, u = i * C::kSteps + step, buf = u % C::kBufs;
         if (!(ok = wait(sm.cw_ready[g][buf], u / C::kBufs))) break;
         tc_fence_after();
-        const uint64_t d = desc_at(dBn, (g * kHalf + step * C::kStep) * 128);
+        const uint64_t d = desc_at(dB, (g * kHalf + step * C::kStep) * 128);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
@@ -337,22 +315,62 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       if (!ok) break;
       umma_commit_elect(smem_addr(&sm.kv_done));
       umma_commit_elect(smem_addr(&sm.empty[tB % NT]));
-      if constexpr (OUT) {
-        if (i + 1 < n && !(ok = scores(i + 1))) break;
+      umma_commit_elect(smem_addr(&sm.empty[tC % NT]));   // its rows have been weighted
+    }
+    if (n > 0) {   // every product and commit has to finish before TMEM is freed
+      umma_commit_elect(smem_addr(&sm.drain[0]));
+      mbar_wait_drain(smem_addr(&sm.drain[0]), 0, p.wait_limit_ns);
+    }
+  } else if (OUT && warp == C::kOutWarp) {
+    // ------------------------------------------- MMA: A Z, P C, and the next chunk's scores
+    constexpr uint32_t kIdescAZ = idesc_az(D), kIdescTS = idesc_ts(D);
+    const uint64_t dZ = smem_desc_sw128(smem_addr(&sm.z[0]), 16, 1024);
+    bool ok = true;
+    auto tile_addr = [&](int t) { return smem_addr(&sm.tile[t % NT][0]); };
+#pragma unroll 1
+    for (int j = 0; j <= n && ok; ++j) {
+      const int i = j - 1;
+      const int tA = i * C::kPerChunk + kTA, tC = i * C::kPerChunk + kTC;
+      if (j > 0) {
+        // A Z, onto the columns the output warps have read for the previous chunk.
+        if (!(ok = wait(sm.z_ready, i))) break;
+        if (i > 0 && !(ok = wait(sm.y_free, i - 1))) break;
+        tc_fence_after();
+        const uint64_t dA = smem_desc_sw128(tile_addr(tA), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_elect(tY, desc_at(dA, (kk >> 2) * kBlk + (kk & 3) * 32),
+                        desc_at(dZ, (kk >> 2) * (D * 128) + (kk & 3) * 32), kIdescAZ, kk > 0);
+        umma_commit_elect(smem_addr(&sm.az_done));
+        umma_commit_elect(smem_addr(&sm.empty[tA % NT]));
         if (!(ok = tile_full(tC))) break;
-        if (!(ok = wait(sm.p_ready, i))) break;   // P written, and A Z scaled: P C adds to it
+        if (!(ok = wait(sm.p_ready, i))) break;   // P written (and A Z scaled): P C adds to A Z
         tc_fence_after();
         const uint64_t dC = smem_desc_sw128(tile_addr(tC), kBlk, 1024);
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
-          umma_ts_elect(tY, tP + kk * 8, desc_at(dC, kk * 2048), kIdescTS, 1u);
+          umma_ts_elect(tY, tS + kk * 8, desc_at(dC, kk * 2048), kIdescTS, 1u);
         umma_commit_elect(smem_addr(&sm.y_full));
+        umma_commit_elect(smem_addr(&sm.empty[tC % NT]));
       }
-      umma_commit_elect(smem_addr(&sm.empty[tC % NT]));
+      if (j < n) {   // scores of chunk j, over the P whose product was issued before
+        const int sA = j * C::kPerChunk + kTA, sB = j * C::kPerChunk + kTB;
+        if (!(ok = tile_full(sA)) || !(ok = tile_full(sB))) break;
+        tc_fence_after();
+        const uint64_t dA = smem_desc_sw128(tile_addr(sA), 16, 1024), dB = smem_desc_sw128(tile_addr(sB), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
+          umma_ss_elect(tS, desc_at(dA, off), desc_at(dB, off), kIdescS, kk > 0);
+        }
+        umma_commit_elect(smem_addr(&sm.s_full));
+        umma_commit_elect(smem_addr(&sm.empty[sA % NT]));
+        umma_commit_elect(smem_addr(&sm.empty[sB % NT]));
+      }
     }
-    if (n > 0) {   // every product and commit has to finish before TMEM is freed
-      umma_commit_elect(smem_addr(&sm.drain));
-      mbar_wait_drain(smem_addr(&sm.drain), 0, p.wait_limit_ns);
+    if (n > 0) {
+      umma_commit_elect(smem_addr(&sm.drain[1]));
+      mbar_wait_drain(smem_addr(&sm.drain[1]), 0, p.wait_limit_ns);
     }
   } else if (warp < 8) {
     // ---------------------- weighted C^T in bf16 terms, and the state; lanes are features of C
@@ -394,99 +412,96 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         }
       }
     }
-    auto publish = [&]() {   // bf16 Z^T for A Z
-      if (busy) {
-#pragma unroll
-        for (int v = 0; v < D / 16; ++v) {
-          const int col = col0 + 8 * v;
-          *reinterpret_cast<uint4*>(&sm.z[(col / 64) * (D * 128) + row * 128 + ((((col % 64) / 8) ^ (row & 7)) * 16)]) =
-              make_uint4(pack_bf16x2(z[8 * v], z[8 * v + 1]), pack_bf16x2(z[8 * v + 2], z[8 * v + 3]),
-                         pack_bf16x2(z[8 * v + 4], z[8 * v + 5]), pack_bf16x2(z[8 * v + 6], z[8 * v + 7]));
-        }
-      }
-      fence_async_smem();
-      warp_arrive(sm.z_ready);
-    };
-    if constexpr (OUT) publish();
     bool ok = true;
-    // Weights this warp's 32 features of one step's tokens into a TMEM buffer.
-    auto weight = [&](int i, int step) {
-      const int tC = i * C::kPerChunk + kTC, u = i * C::kSteps + step, buf = u % C::kBufs;
-      if (step == 0 && !tile_full(tC)) return false;
-      if (u >= C::kBufs && !wait(sm.cw_free[grp][buf], u / C::kBufs - 1)) return false;
-      if (busy) {
-        const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
-        // The features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
-        const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
+    // Steps in order; the state after chunk i is taken kAhead steps into chunk i + 1 (with two
+    // buffers one step is weighted while the tensor core finishes the chunk).
+    constexpr int kAhead = C::kBufs - 1;
+    const int steps = n * C::kSteps;
+    int zi = 0;   // chunks whose state has been added
+#pragma unroll 1
+    for (int u = 0; u < steps + kAhead && ok; ++u) {
+      if (OUT && u == zi * C::kSteps + (zi > 0 ? kAhead : 0) && zi < n) {   // bf16 Z^T for A Z of chunk zi
+        if (zi > 0 && !(ok = wait(sm.az_done, zi - 1))) break;
+        if (busy) {
 #pragma unroll
-        for (int k = 0; k < C::kStep / 16; ++k) {   // 16 tokens at a time
-          const int tok = grp * kHalf + step * C::kStep + 16 * k;
-          uint32_t r[2][4], t[TERMS][2][4];
+          for (int v = 0; v < D / 16; ++v) {
+            const int col = col0 + 8 * v;
+            *reinterpret_cast<uint4*>(
+                &sm.z[(col / 64) * (D * 128) + row * 128 + ((((col % 64) / 8) ^ (row & 7)) * 16)]) =
+                make_uint4(pack_bf16x2(z[8 * v], z[8 * v + 1]), pack_bf16x2(z[8 * v + 2], z[8 * v + 3]),
+                           pack_bf16x2(z[8 * v + 4], z[8 * v + 5]), pack_bf16x2(z[8 * v + 6], z[8 * v + 7]));
+          }
+        }
+        fence_async_smem();
+        warp_arrive(sm.z_ready);
+      }
+      if (u < steps) {
+        // This warp's 32 features of one step's tokens into a TMEM buffer.
+        const int i = u / C::kSteps, step = u % C::kSteps, buf = u % C::kBufs;
+        const int tC = i * C::kPerChunk + kTC;
+        if (step == 0 && !(ok = tile_full(tC))) break;
+        if (u >= C::kBufs && !(ok = wait(sm.cw_free[grp][buf], u / C::kBufs - 1))) break;
+        if (busy) {
+          const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
+          // The features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
+          const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
+#pragma unroll 1
+          for (int k = 0; k < C::kStep / 16; ++k) {   // 16 tokens at a time
+            const int tok = grp * kHalf + step * C::kStep + 16 * k;
+            uint32_t r[2][4], t[TERMS][2][4];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int at = tok + 8 * v + (lane & 7);
-            ldmatrix_x4_trans(src + at * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) * 16), r[v]);
-            const int pair = (tok + 8 * v) / 2 + (lane & 3);   // this lane's two tokens
-            const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
-            if (!whole) {   // rows past the chunk's tokens may hold anything
+            for (int v = 0; v < 2; ++v) {
+              const int at = tok + 8 * v + (lane & 7);
+              ldmatrix_x4_trans(src + at * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) * 16), r[v]);
+              const int pair = (tok + 8 * v) / 2 + (lane & 3);   // this lane's two tokens
+              const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
+              if (!whole) {   // rows past the chunk's tokens may hold anything
 #pragma unroll
-              for (int m = 0; m < 4; ++m)
-                r[v][m] = 2 * pair + 1 < tail ? r[v][m] : 2 * pair < tail ? r[v][m] & 0xffffu : 0u;
-            }
-            const uint64_t ww = f2_pack(w.x, w.y);
+                for (int m = 0; m < 4; ++m)
+                  r[v][m] = 2 * pair + 1 < tail ? r[v][m] : 2 * pair < tail ? r[v][m] & 0xffffu : 0u;
+              }
+              const uint64_t ww = f2_pack(w.x, w.y);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              uint64_t x = f2_mul(bf16x2_to_f2(r[v][m]), ww);
+              for (int m = 0; m < 4; ++m) {
+                uint64_t x = f2_mul(bf16x2_to_f2(r[v][m]), ww);
 #pragma unroll
-              for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
-                float x0, x1;
-                f2_unpack(x, x0, x1);
-                t[e][v][m] = pack_bf16x2(x0, x1);
-                if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][v][m]));
+                for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
+                  float x0, x1;
+                  f2_unpack(x, x0, x1);
+                  t[e][v][m] = pack_bf16x2(x0, x1);
+                  if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][v][m]));
+                }
               }
             }
+            const uint32_t dst = tCw + lane_off + (grp * C::kBufs + buf) * C::kBufCols + 8 * k;
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) {
+              const uint32_t col = dst + e * (C::kStep / 2);
+              tmem_st_16x128b_x2(col, t[e][0][0], t[e][0][1], t[e][1][0], t[e][1][1]);
+              tmem_st_16x128b_x2(col + (16u << 16), t[e][0][2], t[e][0][3], t[e][1][2], t[e][1][3]);
+            }
           }
-          const uint32_t dst = tCw + lane_off + (grp * C::kBufs + buf) * C::kBufCols + 8 * k;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        warp_arrive(sm.cw_ready[grp][buf]);
+      }
+      if (u == (zi + 1) * C::kSteps + kAhead - 1) {   // the state after chunk zi
+        if (!(ok = wait(sm.kv_done, zi))) break;
+        tc_fence_after();
+        const double dl = chunk_at<REV>(p, ci0 + zi).len == kChunk ? d_full : d_tail;
+        const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
+        if (busy) {
 #pragma unroll
-          for (int e = 0; e < TERMS; ++e) {
-            const uint32_t col = dst + e * (C::kStep / 2);
-            tmem_st_16x128b_x2(col, t[e][0][0], t[e][0][1], t[e][1][0], t[e][1][1]);
-            tmem_st_16x128b_x2(col + (16u << 16), t[e][0][2], t[e][0][3], t[e][1][2], t[e][1][3]);
+          for (int q = 0; q < D / 2; q += 32) {
+            uint32_t t0[32];
+            tmem_ld32(tbase + lane_off + col0 + q, t0);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, __uint_as_float(t0[k])));
           }
         }
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      warp_arrive(sm.cw_ready[grp][buf]);
-      return true;
-    };
-    // With two buffers a chunk's first step is weighted before the state of the chunk before
-    // is taken, while the tensor core finishes that.
-    constexpr int kAhead = C::kBufs - 1;
-    for (int step = 0; step < kAhead && n > 0 && ok; ++step) ok = weight(0, step);
-    for (int i = 0; i < n && ok; ++i) {
-      for (int step = kAhead; step < C::kSteps && ok; ++step) ok = weight(i, step);
-      for (int step = 0; step < kAhead && i + 1 < n && ok; ++step) ok = weight(i + 1, step);
-      if (!ok || !(ok = wait(sm.kv_done, i))) break;
-      tc_fence_after();
-      const double dl = chunk_at<REV>(p, ci0 + i).len == kChunk ? d_full : d_tail;
-      const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
-      if (busy) {
-#pragma unroll
-        for (int q = 0; q < D / 2; q += 32) {
-          uint32_t t0[32];
-          tmem_ld32(tbase + lane_off + col0 + q, t0);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, __uint_as_float(t0[k])));
-        }
-      }
-      tc_fence_before();
-      if (i + 1 < n) {
-        warp_arrive(sm.kv_free);
-        if constexpr (OUT) {
-          if (!(ok = wait(sm.az_done, i))) break;
-          publish();
-        }
+        tc_fence_before();
+        if (++zi < n) warp_arrive(sm.kv_free);
       }
     }
     if (ok && busy) {
@@ -507,118 +522,133 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const float ldf = static_cast<float>(ld);
-    // Decay of score (row, 32m + jj), exponent |row - column| >= 0: off the diagonal block
-    // (m != quad) a row factor times a column power, forward d^(row - 32m - 31) d^(31 - jj),
-    // backward d^(32m - row) d^jj; on it d^|lane - jj| from the table.
-    float f[4];
+    // Score (row p, column j) is weighted by d^(p - j) and A Z's row by d^(p + e).
+    // Slow decays: P_pj = S_pj d^(-j - e) adds to A Z as it is, and the row factor d^(p + e)
+    // multiplies the sum. Fast ones, where d^-128 could overflow: d^(p - j) as a row factor
+    // times a column power off the diagonal 32-column block, from a table on it, and A Z is
+    // scaled in place. Either way a block's weights are 32 column powers, kept in registers,
+    // times one factor per block (uniform, or the row's):
+    //                          column power           block factor
+    //   slow   forward         d^-jj                  d^(-32m - 1)
+    //          backward        d^(jj - 31)            d^(-(L - 32 - 32m))
+    //   fast   forward         d^(31 - jj)            d^(row - 32m - 31)
+    //          backward        d^jj                   d^(32m - row)
+    uint64_t off[16];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int x = REV ? 32 * m - row : row - 32 * m - 31;
-      f[m] = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_in : p.s_in;
+    for (int j = 0; j < 16; ++j) {
+      const int up = REV ? 2 * j - 31 : -2 * j;   // of the slow form, at column 2j
+      const int x0 = slow ? up : up + 31, x1 = REV ? x0 + 1 : x0 - 1;
+      off[j] = f2_pack(x0 == 0 ? 1.f : expf(ldf * static_cast<float>(x0)),
+                       x1 == 0 ? 1.f : expf(ldf * static_cast<float>(x1)));
     }
-    const float4* off = reinterpret_cast<const float4*>(&sm.pow32[0]);
     const float* diag = &sm.diag[32 + (REV ? -lane : lane)];   // column jj at REV ? +jj : -jj
-    // The masked blocks of P are zero for good.
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const uint32_t zero[16] = {0u};
-      if (REV ? m < quad : m > quad) tmem_st16(tP + lane_off + 16 * m, zero);
-    }
+    const uint32_t ydst = smem_addr(&sm.y[0][quad][0]) + lane * 128;
+    const int first = REV ? quad : 0, last = REV ? 3 : quad;   // blocks that are not masked whole
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const ChunkAt c = chunk_at<REV>(p, ci0 + i);
+      const int x = REV ? c.len - 1 - row : row + 1;
+      const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
       if (!(ok = wait(sm.s_full, i))) break;
       tc_fence_after();
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (REV ? m < quad : m > quad) continue;
+#pragma unroll 1
+      for (int m = 0; m < 4; ++m) {   // P over the scores: block m's columns were read by block m / 2
         uint32_t s[32], pk[16];
+        if (m < first || m > last) {
+          const uint32_t zero[16] = {0u};
+          tmem_st16(tS + lane_off + 16 * m, zero);
+          continue;
+        }
         tmem_ld32(tS + lane_off + 32 * m, s);
         if (REV && c.len < kChunk) {   // columns past the chunk's tokens hold other rows
 #pragma unroll
           for (int jj = 0; jj < 32; ++jj) s[jj] = 32 * m + jj < c.len ? s[jj] : 0u;
         }
-        const uint64_t ff = f2_pack(f[m], f[m]);
+        if (slow || m != quad) {
+          const int xb = slow ? (REV ? 32 + 32 * m - c.len : -32 * m - 1) : (REV ? 32 * m - row : row - 32 * m - 31);
+          const float fm = expf(ldf * static_cast<float>(xb)) * (slow ? p.s_in / p.s_st : p.s_in);
+          const uint64_t ff = f2_pack(fm, fm);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint64_t w0, w1;
-          if (m == quad) {
-            w0 = f2_pack(diag[REV ? 4 * q : -4 * q], diag[REV ? 4 * q + 1 : -4 * q - 1]);
-            w1 = f2_pack(diag[REV ? 4 * q + 2 : -4 * q - 2], diag[REV ? 4 * q + 3 : -4 * q - 3]);
-          } else {
-            const float4 v = off[REV ? q : 7 - q];
-            w0 = f2_mul(REV ? f2_pack(v.x, v.y) : f2_pack(v.w, v.z), ff);
-            w1 = f2_mul(REV ? f2_pack(v.z, v.w) : f2_pack(v.y, v.x), ff);
+          for (int j = 0; j < 16; ++j) {
+            float x0, x1;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2_mul(off[j], ff)), x0,
+                      x1);
+            pk[j] = pack_bf16x2(x0, x1);
           }
-          float x0, x1;
-          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), w0), x0, x1);
-          pk[2 * q] = pack_bf16x2(x0, x1);
-          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), w1), x0, x1);
-          pk[2 * q + 1] = pack_bf16x2(x0, x1);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            pk[j] = pack_bf16x2(__uint_as_float(s[2 * j]) * diag[REV ? 2 * j : -2 * j],
+                                __uint_as_float(s[2 * j + 1]) * diag[REV ? 2 * j + 1 : -2 * j - 1]);
         }
-        tmem_st16(tP + lane_off + 16 * m, pk);
+        if (m == quad) {   // the masked side of the diagonal block, 0 whatever the scores
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const bool k0 = REV ? 2 * j >= lane : 2 * j <= lane, k1 = REV ? 2 * j + 1 >= lane : 2 * j + 1 <= lane;
+            pk[j] &= (k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u);
+          }
+        }
+        tmem_st16(tS + lane_off + 16 * m, pk);
       }
-      tc_fence_before();
-      warp_arrive(sm.s_free);   // the next chunk's scores may come
-      // A Z, scaled in place by the decay since the chunk's start.
-      const int x = REV ? c.len - 1 - row : row + 1;
-      const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
-      if (!(ok = wait(sm.az_done, i))) break;
-      tc_fence_after();
+      if (!slow) {
+        if (!(ok = wait(sm.az_done, i))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < D; q += 32) {
+          uint32_t az[32];
+          tmem_ld32(tY + lane_off + q, az);
 #pragma unroll
-      for (int q = 0; q < D; q += 32) {
-        uint32_t az[32];
-        tmem_ld32(tY + lane_off + q, az);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) az[k] = __float_as_uint(__uint_as_float(az[k]) * w);
-        tmem_st16(tY + lane_off + q, az);
-        tmem_st16(tY + lane_off + q + 16, az + 16);
+          for (int k = 0; k < 32; ++k) az[k] = __float_as_uint(__uint_as_float(az[k]) * w);
+          tmem_st16(tY + lane_off + q, az);
+          tmem_st16(tY + lane_off + q + 16, az + 16);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(sm.p_ready);
+      // Rows leave through shared memory and TMA stores of 32 rows x 64 columns (a thread's
+      // own stores would touch 32 lines at a time and hold up the other warps' shared-memory
+      // accesses); a warp whose rows end inside the chunk stores them itself, the rows after
+      // may be another piece's.
+      const bool staged = quad * 32 + 32 <= c.len;
+      const int rb = c.rank * p.B + b;
+      __nv_bfloat16* dst = p.y + ((static_cast<int64_t>(rb) * p.T + c.t0 + row) * p.H + h) * D;
+      if (lane == 0) bulk_wait_read<0>();   // the chunk before has left the buffers
       if (!(ok = wait(sm.y_full, i))) break;
       tc_fence_after();
-      uint32_t out[D / 2];
+      const uint64_t wy = slow ? f2_pack(w, w) : f2_pack(1.f, 1.f);
+#pragma unroll 1
+      for (int q = 0; q < C::kBlocks; ++q) {
+        uint32_t y[64];
+        tmem_ld64(tY + lane_off + 64 * q, *reinterpret_cast<uint32_t(*)[32]>(y), *reinterpret_cast<uint32_t(*)[32]>(y + 32));
 #pragma unroll
-      for (int q = 0; q < D; q += 32) {
-        uint32_t y[32];
-        tmem_ld32(tY + lane_off + q, y);
+        for (int k = 0; k < 8; ++k) {
+          uint32_t v[4];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          out[q / 2 + k] = pack_bf16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+          for (int e = 0; e < 4; ++e) {
+            float x0, x1;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(y[8 * k + 2 * e]), __uint_as_float(y[8 * k + 2 * e + 1])), wy), x0,
+                      x1);
+            v[e] = pack_bf16x2(x0, x1);
+          }
+          if (staged) st_shared_v4(ydst + q * (4 * 32 * 128) + ((k ^ (lane & 7)) * 16), v);
+          else if (row < c.len) reinterpret_cast<uint4*>(dst)[8 * q + k] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
       }
       tc_fence_before();
+      fence_async_smem();
       warp_arrive(sm.y_free);
-      // Through shared memory and TMA stores of 32 rows x 64 columns (a thread's own stores
-      // would touch 32 lines at a time and hold up the other warps' shared-memory accesses); a
-      // warp whose rows end inside the chunk stores them itself, the rows after may be another
-      // piece's.
-      if (quad * 32 + 32 <= c.len) {
-        if (lane == 0) bulk_wait_read<0>();   // the chunk before has left the buffers
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          *reinterpret_cast<uint4*>(&sm.y[k / 8][quad][lane * 128 + (((k % 8) ^ (lane & 7)) * 16)]) =
-              make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0)
-          for (int blk = 0; blk < C::kBlocks; ++blk)
-            tma_store_4d(&tm_y, smem_addr(&sm.y[blk][quad][0]), blk * 64, h, c.t0 + quad * 32, c.rank * p.B + b);
-      } else if (row < c.len) {
-        const int64_t tok = static_cast<int64_t>(c.rank * p.B + b) * p.T + c.t0 + row;
-        uint4* dst = reinterpret_cast<uint4*>(p.y + (tok * p.H + h) * D);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-      }
+      if (staged && lane == 0)
+        for (int blk = 0; blk < C::kBlocks; ++blk)
+          tma_store_4d(&tm_y, smem_addr(&sm.y[blk][quad][0]), blk * 64, h, c.t0 + quad * 32, rb);
     }
     if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kMmaWarp) {
+  if (warp == C::kKvWarp) {
     tc_fence_after();
     tmem_dealloc(tbase, C::kTmemCols);
   }
