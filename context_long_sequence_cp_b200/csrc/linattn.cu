@@ -142,32 +142,41 @@ __device__ __forceinline__ double decay_pow(double ld, int64_t n) {
   return n == 0 ? 1.0 : exp(ld * static_cast<double>(n));
 }
 
-// Chunk ci in walking order: where its rows are.
-struct ChunkAt {
-  int rank, t0, len;
-  int before;   // tokens walked before it
-};
+// The chunks in walking order: where a chunk's rows are. Moved on by counting, since the
+// divisions would sit in every role's way once per chunk.
 template <bool REV>
-__device__ __forceinline__ ChunkAt chunk_at(const LinParams& p, int ci) {
-  const int cn = REV ? p.nch - 1 - ci : ci;
-  const int piece = cn / p.chunks_per_piece;
-  const int off = (cn - piece * p.chunks_per_piece) * kChunk;
-  ChunkAt c;
-  c.len = min(kChunk, p.piece_len - off);
-  if (!p.zigzag) {
-    c.rank = piece;
-    c.t0 = off;
-  } else {
-    c.rank = piece < p.N ? piece : 2 * p.N - 1 - piece;
-    c.t0 = (piece < p.N ? 0 : p.piece_len) + off;
+struct ChunkWalk {
+  int piece, off, len;
+  __device__ __forceinline__ ChunkWalk(const LinParams& p, int ci) {
+    const int cn = REV ? p.nch - 1 - ci : ci;
+    piece = cn / p.chunks_per_piece;
+    off = (cn - piece * p.chunks_per_piece) * kChunk;
+    len = min(kChunk, p.piece_len - off);
   }
-  const int p0 = piece * p.piece_len + off;
-  c.before = REV ? p.S - p0 - c.len : p0;
-  return c;
-}
+  __device__ __forceinline__ void next(const LinParams& p) {
+    off += REV ? -kChunk : kChunk;
+    if (REV ? off < 0 : off >= p.piece_len) {
+      piece += REV ? -1 : 1;
+      off = REV ? (p.chunks_per_piece - 1) * kChunk : 0;
+    }
+    len = min(kChunk, p.piece_len - off);
+  }
+  __device__ __forceinline__ bool whole() const { return len == kChunk; }
+  // Zigzag: rank r holds piece r, then piece 2N - 1 - r.
+  __device__ __forceinline__ int rank(const LinParams& p) const {
+    return !p.zigzag || piece < p.N ? piece : 2 * p.N - 1 - piece;
+  }
+  __device__ __forceinline__ int token(const LinParams& p) const {   // first row, within the rank
+    return (!p.zigzag || piece < p.N ? 0 : p.piece_len) + off;
+  }
+};
+// Tokens walked before chunk ci.
 template <bool REV>
 __device__ __forceinline__ int walked_before(const LinParams& p, int ci) {
-  return ci >= p.nch ? p.S : chunk_at<REV>(p, ci).before;
+  if (ci >= p.nch) return p.S;
+  const ChunkWalk<REV> c(p, ci);
+  const int p0 = c.piece * p.piece_len + c.off;
+  return REV ? p.S - p0 - c.len : p0;
 }
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
@@ -261,19 +270,18 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     bool ok = true;
     int t = 0;
     // The ring holds less than two chunks, so the one after next is brought into L2 ahead.
-    auto prefetch = [&](int i) {
-      if (i >= n) return;
-      const ChunkAt c = chunk_at<REV>(p, ci0 + i);
+    ChunkWalk<REV> ahead(p, ci0), c = ahead;
+    auto prefetch = [&]() {
+      ahead.next(p);
+      const int rb = ahead.rank(p) * p.B + b, t0 = ahead.token(p);
       for (int which = 0; which < C::kPerChunk; ++which)
         for (int blk = 0; blk < C::kBlocks; ++blk)
-          tma_prefetch_4d_elect(which == kTC ? &tm_c : which == kTB ? &tm_b : &tm_a, blk * 64, h, c.t0,
-                                c.rank * p.B + b);
+          tma_prefetch_4d_elect(which == kTC ? &tm_c : which == kTB ? &tm_b : &tm_a, blk * 64, h, t0, rb);
     };
-    prefetch(1);
-    for (int i = 0; i < n && ok; ++i) {
-      const ChunkAt c = chunk_at<REV>(p, ci0 + i);
-      const int rb = c.rank * p.B + b;
-      prefetch(i + 2);
+    if (n > 1) prefetch();
+    for (int i = 0; i < n && ok; ++i, c.next(p)) {
+      const int rb = c.rank(p) * p.B + b, t0 = c.token(p);
+      if (i + 2 < n) prefetch();
       for (int which = 0; which < C::kPerChunk; ++which, ++t) {
         const int st = t % NT;
         if (t >= NT && !(ok = wait(sm.empty[st], t / NT - 1))) break;
@@ -281,7 +289,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         const CUtensorMap* map = which == kTC ? &tm_c : which == kTB ? &tm_b : &tm_a;
         mbar_arrive_expect_tx_elect(bar, C::kTileBytes);
         for (int blk = 0; blk < C::kBlocks; ++blk)
-          tma_load_4d_elect(smem_addr(&sm.tile[st][0]) + blk * kBlk, map, bar, blk * 64, h, c.t0, rb, pol);
+          tma_load_4d_elect(smem_addr(&sm.tile[st][0]) + blk * kBlk, map, bar, blk * 64, h, t0, rb, pol);
       }
     }
     if (!ok)   // abort: let every load this warp issued land before the CTA exits
@@ -380,6 +388,8 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     const bool busy = quad * 32 < D;           // warp-uniform; for D = 64 two quads have no rows
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const double d_full = decay_pow(ld, kChunk), d_tail = decay_pow(ld, tail);
+    const float hi_full = static_cast<float>(d_full), lo_full = static_cast<float>(d_full - static_cast<double>(hi_full));
+    const float hi_tail = static_cast<float>(d_tail), lo_tail = static_cast<float>(d_tail - static_cast<double>(hi_tail));
     float z[D / 2];
 #pragma unroll
     for (int q = 0; q < D / 2; ++q) z[q] = 0.f;
@@ -417,6 +427,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     // buffers one step is weighted while the tensor core finishes the chunk).
     constexpr int kAhead = C::kBufs - 1;
     const int steps = n * C::kSteps;
+    ChunkWalk<REV> cv(p, ci0), cz = cv;   // chunk being weighted, chunk whose state is taken
     int zi = 0;   // chunks whose state has been added
 #pragma unroll 1
     for (int u = 0; u < steps + kAhead && ok; ++u) {
@@ -442,7 +453,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         if (step == 0 && !(ok = tile_full(tC))) break;
         if (u >= C::kBufs && !(ok = wait(sm.cw_free[grp][buf], u / C::kBufs - 1))) break;
         if (busy) {
-          const bool whole = chunk_at<REV>(p, ci0 + i).len == kChunk;
+          const bool whole = cv.whole();
           // The features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
           const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
 #pragma unroll 1
@@ -485,12 +496,13 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         }
         tc_fence_before();
         warp_arrive(sm.cw_ready[grp][buf]);
+        if (step == C::kSteps - 1) cv.next(p);
       }
       if (u == (zi + 1) * C::kSteps + kAhead - 1) {   // the state after chunk zi
         if (!(ok = wait(sm.kv_done, zi))) break;
         tc_fence_after();
-        const double dl = chunk_at<REV>(p, ci0 + zi).len == kChunk ? d_full : d_tail;
-        const float hi = static_cast<float>(dl), lo = static_cast<float>(dl - static_cast<double>(hi));
+        const float hi = cz.whole() ? hi_full : hi_tail, lo = cz.whole() ? lo_full : lo_tail;
+        cz.next(p);
         if (busy) {
 #pragma unroll
           for (int q = 0; q < D / 2; q += 32) {
@@ -545,15 +557,18 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     const uint32_t ydst = smem_addr(&sm.y[0][quad][0]) + lane * 128;
     const int first = REV ? quad : 0, last = REV ? 3 : quad;   // blocks that are not masked whole
     bool ok = true;
+    ChunkWalk<REV> c(p, ci0);
+    const float up32 = slow ? expf(ldf * (REV ? 32.f : -32.f)) : 1.f;
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const ChunkAt c = chunk_at<REV>(p, ci0 + i);
+    for (int i = 0; i < n; ++i, c.next(p)) {
+      // d^(p + e) of this row, and the slow form's factor of the first block.
       const int x = REV ? c.len - 1 - row : row + 1;
       const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
+      float fs = expf(ldf * static_cast<float>(REV ? 32 - c.len : -1)) * (p.s_in / p.s_st);
       if (!(ok = wait(sm.s_full, i))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int m = 0; m < 4; ++m) {   // P over the scores: block m's columns were read by block m / 2
+      for (int m = 0; m < 4; ++m, fs *= up32) {   // P over the scores: block m's columns were read by block m / 2
         uint32_t s[32], pk[16];
         if (m < first || m > last) {
           const uint32_t zero[16] = {0u};
@@ -566,8 +581,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
           for (int jj = 0; jj < 32; ++jj) s[jj] = 32 * m + jj < c.len ? s[jj] : 0u;
         }
         if (slow || m != quad) {
-          const int xb = slow ? (REV ? 32 + 32 * m - c.len : -32 * m - 1) : (REV ? 32 * m - row : row - 32 * m - 31);
-          const float fm = expf(ldf * static_cast<float>(xb)) * (slow ? p.s_in / p.s_st : p.s_in);
+          const float fm = slow ? fs : expf(ldf * static_cast<float>(REV ? 32 * m - row : row - 32 * m - 31)) * p.s_in;
           const uint64_t ff = f2_pack(fm, fm);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -612,8 +626,8 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       // accesses); a warp whose rows end inside the chunk stores them itself, the rows after
       // may be another piece's.
       const bool staged = quad * 32 + 32 <= c.len;
-      const int rb = c.rank * p.B + b;
-      __nv_bfloat16* dst = p.y + ((static_cast<int64_t>(rb) * p.T + c.t0 + row) * p.H + h) * D;
+      const int rb = c.rank(p) * p.B + b, t0 = c.token(p);
+      __nv_bfloat16* dst = p.y + ((static_cast<int64_t>(rb) * p.T + t0 + row) * p.H + h) * D;
       if (lane == 0) bulk_wait_read<0>();   // the chunk before has left the buffers
       if (!(ok = wait(sm.y_full, i))) break;
       tc_fence_after();
@@ -641,7 +655,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       warp_arrive(sm.y_free);
       if (staged && lane == 0)
         for (int blk = 0; blk < C::kBlocks; ++blk)
-          tma_store_4d(&tm_y, smem_addr(&sm.y[blk][quad][0]), blk * 64, h, c.t0 + quad * 32, rb);
+          tma_store_4d(&tm_y, smem_addr(&sm.y[blk][quad][0]), blk * 64, h, t0 + quad * 32, rb);
     }
     if (lane == 0) bulk_wait_all();
   }
