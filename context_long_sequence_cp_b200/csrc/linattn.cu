@@ -144,20 +144,19 @@ __device__ __forceinline__ double decay_pow(double ld, int64_t n) {
 
 // The chunks in walking order: where a chunk's rows are. Moved on by counting, since the
 // divisions would sit in every role's way once per chunk.
-template <bool REV>
 struct ChunkWalk {
   int piece, off, len;
   __device__ __forceinline__ ChunkWalk(const LinParams& p, int ci) {
-    const int cn = REV ? p.nch - 1 - ci : ci;
+    const int cn = p.reverse ? p.nch - 1 - ci : ci;
     piece = cn / p.chunks_per_piece;
     off = (cn - piece * p.chunks_per_piece) * kChunk;
     len = min(kChunk, p.piece_len - off);
   }
   __device__ __forceinline__ void next(const LinParams& p) {
-    off += REV ? -kChunk : kChunk;
-    if (REV ? off < 0 : off >= p.piece_len) {
-      piece += REV ? -1 : 1;
-      off = REV ? (p.chunks_per_piece - 1) * kChunk : 0;
+    off += p.reverse ? -kChunk : kChunk;
+    if (off < 0 || off >= p.piece_len) {
+      piece += p.reverse ? -1 : 1;
+      off = p.reverse ? (p.chunks_per_piece - 1) * kChunk : 0;
     }
     len = min(kChunk, p.piece_len - off);
   }
@@ -171,12 +170,11 @@ struct ChunkWalk {
   }
 };
 // Tokens walked before chunk ci.
-template <bool REV>
 __device__ __forceinline__ int walked_before(const LinParams& p, int ci) {
   if (ci >= p.nch) return p.S;
-  const ChunkWalk<REV> c(p, ci);
+  const ChunkWalk c(p, ci);
   const int p0 = c.piece * p.piece_len + c.off;
-  return REV ? p.S - p0 - c.len : p0;
+  return p.reverse ? p.S - p0 - c.len : p0;
 }
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
@@ -192,11 +190,21 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-template <int D, bool OUT, bool REV, int TERMS>
+// One CTA per (scan, segment, batch, head). The backward's three scans are one launch: they
+// are independent, so their CTAs fill the waves together, and those of one place in the
+// sequence, which read the same rows, run next to each other. The direction is a run-time
+// flag: as a template parameter it put three copies of the code side by side on the GPU, and
+// a chunk took twice as long for want of instructions.
+template <int D, bool OUT, int TERMS>
 __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
-    linattn_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y,
-                   const __grid_constant__ LinParams p) {
+    linattn_kernel(const __grid_constant__ LinLaunch launch) {
+  const LinScan& L = launch.scan[blockIdx.x % launch.scans];
+  const LinParams& p = L.p;
+  const CUtensorMap &tm_a = L.tm_a, &tm_b = L.tm_b, &tm_c = L.tm_c, &tm_y = L.tm_y;
+  const bool back = p.reverse;
+  const int place = static_cast<int>(blockIdx.x) / launch.scans;
+  const int bh = place % p.units;
+  const int seg = OUT && back ? p.nseg - 1 - place / p.units : place / p.units;   // in walking order
   using C = LinCfg<D, OUT, TERMS>;
   constexpr int NT = C::kTiles;
   // Order of a chunk's tiles in the ring: A is the first to be free, so the next chunk's A and B
@@ -207,8 +215,6 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int bh = static_cast<int>(blockIdx.x) % p.units;
-  const int seg = static_cast<int>(blockIdx.x) / p.units;
   const int h = bh % p.H, b = bh / p.H;
   const int ci0 = static_cast<int>(static_cast<int64_t>(seg) * p.nch / p.nseg);
   const int ci1 = static_cast<int>(static_cast<int64_t>(seg + 1) * p.nch / p.nseg);
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     sm.diag[threadIdx.x] = threadIdx.x < 32 ? 0.f : static_cast<float>(decay_pow(ld, threadIdx.x - 32)) * p.s_in;
   if (threadIdx.x < 256) {
     const int r = threadIdx.x & 127, len = threadIdx.x < 128 ? kChunk : tail;
-    const float w = r < len ? static_cast<float>(decay_pow(ld, REV ? r + 1 : len - 1 - r)) * p.s_upd : 0.f;
+    const float w = r < len ? static_cast<float>(decay_pow(ld, back ? r + 1 : len - 1 - r)) * p.s_upd : 0.f;
     reinterpret_cast<float*>(threadIdx.x < 128 ? sm.w_full : sm.w_tail)[r] = w;
   }
   if (warp == C::kKvWarp) {
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     bool ok = true;
     int t = 0;
     // The ring holds less than two chunks, so the one after next is brought into L2 ahead.
-    ChunkWalk<REV> ahead(p, ci0), c = ahead;
+    ChunkWalk ahead(p, ci0), c = ahead;
     auto prefetch = [&]() {
       ahead.next(p);
       const int rb = ahead.rank(p) * p.B + b, t0 = ahead.token(p);
@@ -388,8 +394,9 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     const bool busy = quad * 32 < D;           // warp-uniform; for D = 64 two quads have no rows
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const double d_full = decay_pow(ld, kChunk), d_tail = decay_pow(ld, tail);
-    const float hi_full = static_cast<float>(d_full), lo_full = static_cast<float>(d_full - static_cast<double>(hi_full));
-    const float hi_tail = static_cast<float>(d_tail), lo_tail = static_cast<float>(d_tail - static_cast<double>(hi_tail));
+    const float hi_full = static_cast<float>(d_full), hi_tail = static_cast<float>(d_tail);
+    const float lo_full = static_cast<float>(d_full - static_cast<double>(hi_full));
+    const float lo_tail = static_cast<float>(d_tail - static_cast<double>(hi_tail));
     float z[D / 2];
 #pragma unroll
     for (int q = 0; q < D / 2; ++q) z[q] = 0.f;
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     // q * 2D + group * D + row, so that a warp's accesses are contiguous.
     const int zt = grp * D + row;
     if (OUT && busy) {
-      const int x = walked_before<REV>(p, ci0);
+      const int x = walked_before(p, ci0);
       if (p.z0 != nullptr) {
         const float w = static_cast<float>(decay_pow(ld, x));
 #pragma unroll
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         }
       }
       for (int g = 0; g < seg; ++g) {
-        const int end = walked_before<REV>(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
+        const int end = walked_before(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
         const float w = x == end ? 1.f : expf(static_cast<float>(ld * (x - end)));
         const float4* src = reinterpret_cast<const float4*>(
                                 p.zseg + (static_cast<int64_t>(bh) * (p.nseg - 1) + g) * (D * D)) + zt;
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     // buffers one step is weighted while the tensor core finishes the chunk).
     constexpr int kAhead = C::kBufs - 1;
     const int steps = n * C::kSteps;
-    ChunkWalk<REV> cv(p, ci0), cz = cv;   // chunk being weighted, chunk whose state is taken
+    ChunkWalk cv(p, ci0), cz = cv;   // chunk being weighted, chunk whose state is taken
     int zi = 0;   // chunks whose state has been added
 #pragma unroll 1
     for (int u = 0; u < steps + kAhead && ok; ++u) {
@@ -548,23 +555,25 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     uint64_t off[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const int up = REV ? 2 * j - 31 : -2 * j;   // of the slow form, at column 2j
-      const int x0 = slow ? up : up + 31, x1 = REV ? x0 + 1 : x0 - 1;
+      const int up = back ? 2 * j - 31 : -2 * j;   // of the slow form, at column 2j
+      const int x0 = slow ? up : up + 31, x1 = back ? x0 + 1 : x0 - 1;
       off[j] = f2_pack(x0 == 0 ? 1.f : expf(ldf * static_cast<float>(x0)),
                        x1 == 0 ? 1.f : expf(ldf * static_cast<float>(x1)));
     }
-    const float* diag = &sm.diag[32 + (REV ? -lane : lane)];   // column jj at REV ? +jj : -jj
+    const int step = back ? 1 : -1;
+    const float* diag = &sm.diag[32 - lane * step];   // column jj at step * jj
     const uint32_t ydst = smem_addr(&sm.y[0][quad][0]) + lane * 128;
-    const int first = REV ? quad : 0, last = REV ? 3 : quad;   // blocks that are not masked whole
+    const int first = back ? quad : 0, last = back ? 3 : quad;   // blocks that are not masked whole
     bool ok = true;
-    ChunkWalk<REV> c(p, ci0);
-    const float up32 = slow ? expf(ldf * (REV ? 32.f : -32.f)) : 1.f;
+    const uint32_t keep = back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // columns of the diagonal block
+    ChunkWalk c(p, ci0);
+    const float up32 = slow ? expf(ldf * (back ? 32.f : -32.f)) : 1.f;
 #pragma unroll 1
     for (int i = 0; i < n; ++i, c.next(p)) {
       // d^(p + e) of this row, and the slow form's factor of the first block.
-      const int x = REV ? c.len - 1 - row : row + 1;
+      const int x = back ? c.len - 1 - row : row + 1;
       const float w = x > 0 ? expf(ldf * static_cast<float>(x)) * p.s_st : p.s_st;
-      float fs = expf(ldf * static_cast<float>(REV ? 32 - c.len : -1)) * (p.s_in / p.s_st);
+      float fs = expf(ldf * static_cast<float>(back ? 32 - c.len : -1)) * (p.s_in / p.s_st);
       if (!(ok = wait(sm.s_full, i))) break;
       tc_fence_after();
 #pragma unroll 1
@@ -576,12 +585,12 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
           continue;
         }
         tmem_ld32(tS + lane_off + 32 * m, s);
-        if (REV && c.len < kChunk) {   // columns past the chunk's tokens hold other rows
+        if (back && c.len < kChunk) {   // columns past the chunk's tokens hold other rows
 #pragma unroll
           for (int jj = 0; jj < 32; ++jj) s[jj] = 32 * m + jj < c.len ? s[jj] : 0u;
         }
         if (slow || m != quad) {
-          const float fm = slow ? fs : expf(ldf * static_cast<float>(REV ? 32 * m - row : row - 32 * m - 31)) * p.s_in;
+          const float fm = slow ? fs : expf(ldf * static_cast<float>(back ? 32 * m - row : row - 32 * m - 31)) * p.s_in;
           const uint64_t ff = f2_pack(fm, fm);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -593,14 +602,13 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            pk[j] = pack_bf16x2(__uint_as_float(s[2 * j]) * diag[REV ? 2 * j : -2 * j],
-                                __uint_as_float(s[2 * j + 1]) * diag[REV ? 2 * j + 1 : -2 * j - 1]);
+            pk[j] = pack_bf16x2(__uint_as_float(s[2 * j]) * diag[2 * j * step],
+                                __uint_as_float(s[2 * j + 1]) * diag[(2 * j + 1) * step]);
         }
         if (m == quad) {   // the masked side of the diagonal block, 0 whatever the scores
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const bool k0 = REV ? 2 * j >= lane : 2 * j <= lane, k1 = REV ? 2 * j + 1 >= lane : 2 * j + 1 <= lane;
-            pk[j] &= (k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u);
+            pk[j] &= (keep & (1u << (2 * j)) ? 0xffffu : 0u) | (keep & (2u << (2 * j)) ? 0xffff0000u : 0u);
           }
         }
         tmem_st16(tS + lane_off + 16 * m, pk);
@@ -635,7 +643,8 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
 #pragma unroll 1
       for (int q = 0; q < C::kBlocks; ++q) {
         uint32_t y[64];
-        tmem_ld64(tY + lane_off + 64 * q, *reinterpret_cast<uint32_t(*)[32]>(y), *reinterpret_cast<uint32_t(*)[32]>(y + 32));
+        tmem_ld64(tY + lane_off + 64 * q, *reinterpret_cast<uint32_t(*)[32]>(y),
+                  *reinterpret_cast<uint32_t(*)[32]>(y + 32));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           uint32_t v[4];
@@ -737,28 +746,29 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
   for (int r = 0; r < RPT; ++r) *reinterpret_cast<float4*>(st + static_cast<int64_t>(rg + r * RG) * D) = s[r];
 }
 
-template <int D, bool OUT, bool REV, int TERMS>
-cudaError_t launch_lin(const LinLaunch& L, int grid, cudaStream_t stream) {
+template <int D, bool OUT, int TERMS>
+bool launch_lin(const LinLaunch& L, int segments, cudaStream_t stream) {
   const size_t smem = sizeof(LinSmem<D, OUT, TERMS>) + 1024;
-  auto kern = linattn_kernel<D, OUT, REV, TERMS>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  kern<<<grid, LinCfg<D, OUT, TERMS>::kThreads, smem, stream>>>(L.tm_a, L.tm_b, L.tm_c, L.tm_y, L.p);
-  return cudaGetLastError();
+  auto kern = linattn_kernel<D, OUT, TERMS>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return false;
+  kern<<<L.scans * L.scan[0].p.units * segments, LinCfg<D, OUT, TERMS>::kThreads, smem, stream>>>(L);
+  return cudaGetLastError() == cudaSuccess;
 }
 
-// The launches of one scan: the segments' own states (all but the last), then the rows.
-template <int D, bool REV, int TERMS>
-bool launch_scan(const LinLaunch& L, cudaStream_t stream) {
-  const LinParams& p = L.p;
-  if (p.nseg > 1 && launch_lin<D, false, REV, TERMS>(L, p.units * (p.nseg - 1), stream) != cudaSuccess) return false;
-  return launch_lin<D, true, REV, TERMS>(L, p.units * p.nseg, stream) == cudaSuccess;
+// The launches of a forward or a backward: the segments' own states (all but the last),
+// then the rows.
+template <int D, int TERMS>
+bool launch_scans(const LinLaunch& L, cudaStream_t stream) {
+  const int nseg = L.scan[0].p.nseg;
+  if (nseg > 1 && !launch_lin<D, false, TERMS>(L, nseg - 1, stream)) return false;
+  return launch_lin<D, true, TERMS>(L, nseg, stream);
 }
-template <int D>
-bool launch_scan(const LinLaunch& L, cudaStream_t stream) {
-  if (L.p.z_out != nullptr) return L.p.reverse ? launch_scan<D, true, 3>(L, stream) : launch_scan<D, false, 3>(L, stream);
-  return L.p.reverse ? launch_scan<D, true, 2>(L, stream) : launch_scan<D, false, 2>(L, stream);
+bool launch_scans(const LinLaunch& L, int D, cudaStream_t stream) {
+  bool exact = false;   // a last state is asked for
+  for (int i = 0; i < L.scans; ++i) exact = exact || L.scan[i].p.z_out != nullptr;
+  if (D == 128) return exact ? launch_scans<128, 3>(L, stream) : launch_scans<128, 2>(L, stream);
+  return exact ? launch_scans<64, 3>(L, stream) : launch_scans<64, 2>(L, stream);
 }
 
 // ------------------------------------------------------------------------ host side
@@ -781,21 +791,20 @@ LinView lin_view(const PlanView& v) {
   return w;
 }
 
-// Segments a sequence is cut into. Modelled time, in chunks of the output launch:
-// waves x chunks per segment, the state launch at half a chunk each, and a fixed cost
-// per launch and wave (pipeline fill). More than kMaxSegments joins too many states.
+// Segments a sequence is cut into, for `ctas` scans x (batch, head) of nch chunks. Modelled
+// time in chunks of the output launch (3.1 us each): a wave costs its chunks, about 2.5 more
+// to fill and drain, and 0.35 for each earlier segment's state to join; a chunk of the state
+// launch 0.45. On 32 heads of 256 chunks (148 SMs) 4 segments take 362 us, 3 take 446, 9 take
+// 375, 2 take 652, and the model orders them so.
 constexpr int kMaxSegments = 64;
-int choose_segments(int units, int nch, int sms) {
+int choose_segments(int64_t ctas, int nch, int sms) {
   int best = 1;
   double best_cost = 0;
   for (int s = 1; s <= nch && s <= kMaxSegments; ++s) {
     const double per = (nch + s - 1) / s;
-    const double waves = (static_cast<int64_t>(units) * s + sms - 1) / sms;
-    double cost = waves * (per + 4.0);
-    if (s > 1) {
-      const double w1 = (static_cast<int64_t>(units) * (s - 1) + sms - 1) / sms;
-      cost += w1 * (0.5 * per + 4.0) + 0.1 * s;
-    }
+    const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
+    double cost = waves * (per + 2.5 + 0.35 * (s - 1));
+    if (s > 1) cost += static_cast<double>((ctas * (s - 1) + sms - 1) / sms) * (0.45 * per + 2.0);
     if (s == 1 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -804,11 +813,14 @@ int choose_segments(int units, int nch, int sms) {
   return best;
 }
 
-size_t scan_workspace(const PlanView& v) {
-  const LinView w = lin_view(v);
-  const int units = v.B * v.H;
-  const int nseg = choose_segments(units, w.nch, v.sms);
-  return static_cast<size_t>(units) * (nseg - 1) * v.D * v.D * sizeof(float);
+size_t state_bytes(const PlanView& v, int nseg) {   // the segments' own states of one scan
+  return static_cast<size_t>(v.B) * v.H * (nseg - 1) * v.D * v.D * sizeof(float);
+}
+size_t fwd_workspace(const PlanView& v) {
+  return state_bytes(v, choose_segments(static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
+}
+size_t bwd_workspace(const PlanView& v) {
+  return 3 * state_bytes(v, choose_segments(3 * static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
 }
 
 struct ScanCall {
@@ -820,16 +832,15 @@ struct ScanCall {
   float* z_out;
 };
 
-int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float* ws, cudaStream_t stream) {
+bool make_scan(LinScan* L, const PlanView& v, const ScanCall& s, const float* log_decay, float* ws, int nseg) {
   const LinView w = lin_view(v);
-  LinLaunch L;
   const int64_t rb = static_cast<int64_t>(w.N) * v.B;
-  if (!encode_map_4d(&L.tm_a, s.a, v.D, v.H, w.T, rb, 1, kChunk) ||
-      !encode_map_4d(&L.tm_b, s.b, v.D, v.H, w.T, rb, 1, kChunk) ||
-      !encode_map_4d(&L.tm_c, s.c, v.D, v.H, w.T, rb, 1, kChunk) ||
-      !encode_map_4d(&L.tm_y, s.y, v.D, v.H, w.T, rb, 1, 32))
-    return CP_ERR_CUDA;
-  LinParams& p = L.p;
+  if (!encode_map_4d(&L->tm_a, s.a, v.D, v.H, w.T, rb, 1, kChunk) ||
+      !encode_map_4d(&L->tm_b, s.b, v.D, v.H, w.T, rb, 1, kChunk) ||
+      !encode_map_4d(&L->tm_c, s.c, v.D, v.H, w.T, rb, 1, kChunk) ||
+      !encode_map_4d(&L->tm_y, s.y, v.D, v.H, w.T, rb, 1, 32))
+    return false;
+  LinParams& p = L->p;
   p.B = v.B;
   p.H = v.H;
   p.S = v.S;
@@ -840,9 +851,9 @@ int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float
   p.chunks_per_piece = w.chunks_per_piece;
   p.nch = w.nch;
   p.units = v.B * v.H;
-  p.nseg = choose_segments(p.units, w.nch, v.sms);
-  p.reverse = s.reverse;
+  p.nseg = nseg;
   p.z0_transposed = s.z0_transposed;
+  p.reverse = s.reverse;
   p.s_in = s.s_in;
   p.s_st = s.s_st;
   p.s_upd = s.s_upd;
@@ -853,8 +864,7 @@ int run_scan(const PlanView& v, const ScanCall& s, const float* log_decay, float
   p.y = static_cast<__nv_bfloat16*>(s.y);
   p.status = v.status;
   p.wait_limit_ns = kWaitLimitNs;
-  const bool ok = v.D == 128 ? launch_scan<128>(L, stream) : launch_scan<64>(L, stream);
-  return ok ? CP_OK : CP_ERR_CUDA;
+  return true;
 }
 
 // Arguments common to the forward and the backward.
@@ -862,8 +872,8 @@ int check_plan(cp_attn_plan_t plan, PlanView* v) {
   const int rc = plan_view(plan, v);
   if (rc != CP_OK) return rc;
   if (v->layout == CP_LAYOUT_ULYSSES || !v->causal) return CP_ERR_UNSUPPORTED;
-  // one CTA per (batch, head) and segment, indexed in int32
-  if (static_cast<int64_t>(v->B) * v->H > (int64_t(1) << 30) / kMaxSegments) return CP_ERR_UNSUPPORTED;
+  // one CTA per scan, (batch, head) and segment, indexed in int32
+  if (static_cast<int64_t>(v->B) * v->H > (int64_t(1) << 29) / kMaxSegments) return CP_ERR_UNSUPPORTED;
   return CP_OK;
 }
 
@@ -878,7 +888,8 @@ extern "C" {
 size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan) {
   PlanView v;
   if (plan == nullptr || check_plan(plan, &v) != CP_OK) return 0;
-  return scan_workspace(v);
+  const size_t f = fwd_workspace(v), b = bwd_workspace(v);
+  return f > b ? f : b;
 }
 
 int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
@@ -892,9 +903,14 @@ int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   PlanView pv;
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
-  if (workspace == nullptr && scan_workspace(pv) > 0) return CP_ERR_WORKSPACE;
-  const ScanCall s = {q, k, v, o, state_in, false, false, pv.scale, pv.scale, 1.f, state_out};
-  return run_scan(pv, s, log_decay, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
+  if (workspace == nullptr && fwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
+  const int nseg = choose_segments(static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
+  LinLaunch L;
+  L.scans = 1;
+  if (!make_scan(&L.scan[0], pv, {q, k, v, o, state_in, false, false, pv.scale, pv.scale, 1.f, state_out}, log_decay,
+                 static_cast<float*>(workspace), nseg))
+    return CP_ERR_CUDA;
+  return launch_scans(L, pv.D, static_cast<cudaStream_t>(stream)) ? CP_OK : CP_ERR_CUDA;
 }
 
 int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
@@ -911,16 +927,20 @@ int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   PlanView pv;
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
-  if (workspace == nullptr && scan_workspace(pv) > 0) return CP_ERR_WORKSPACE;
-  float* ws = static_cast<float*>(workspace);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (workspace == nullptr && bwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
+  const int nseg = choose_segments(3 * static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
+  const size_t part = state_bytes(pv, nseg) / sizeof(float);
   const float sc = pv.scale;
   const ScanCall calls[3] = {{dout, v, k, dq, state_in, true, false, sc, sc, 1.f, nullptr},
                              {v, dout, q, dk, dstate_out, true, true, sc, 1.f, sc, nullptr},
                              {k, q, dout, dv, dstate_out, false, true, sc, 1.f, sc, dstate_in}};
-  for (const ScanCall& s : calls)   // one after the other on the stream: they share the workspace
-    if ((rc = run_scan(pv, s, log_decay, ws, st)) != CP_OK) return rc;
-  return CP_OK;
+  LinLaunch L;
+  L.scans = 3;
+  for (int i = 0; i < 3; ++i) {
+    float* ws = part > 0 ? static_cast<float*>(workspace) + i * part : nullptr;
+    if (!make_scan(&L.scan[i], pv, calls[i], log_decay, ws, nseg)) return CP_ERR_CUDA;
+  }
+  return launch_scans(L, pv.D, static_cast<cudaStream_t>(stream)) ? CP_OK : CP_ERR_CUDA;
 }
 
 int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, const void* v, const float* log_decay,

@@ -29,9 +29,14 @@ struct LinParams {
   uint64_t wait_limit_ns;
 };
 
-struct LinLaunch {
+struct LinScan {
   CUtensorMap tm_a, tm_b, tm_c, tm_y;   // 4-D views (D, H, T, N*B)
   LinParams p;
+};
+
+struct LinLaunch {
+  LinScan scan[3];   // the forward's one, or the backward's three
+  int scans;
 };
 
 constexpr int kLinStepMaxT = 16;   // tokens of one recurrent call
