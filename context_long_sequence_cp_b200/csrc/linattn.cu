@@ -114,12 +114,9 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                : "r"(addr)
                : "memory");
 }
-// 16 lanes x 8 columns of TMEM from two pairs of such fragments: registers 2k and 2k + 1
-// hold lanes t / 4 and 8 + t / 4 of column 4k + t % 4.
-__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r0), "r"(r1), "r"(r2),
-               "r"(r3)
-               : "memory");
+// 16 lanes x 4 columns of TMEM from two such fragments: lanes t / 4 and 8 + t / 4 of column t % 4.
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, uint32_t r0, uint32_t r1) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r0), "r"(r1) : "memory");
 }
 
 // TMA store of a box from shared memory, one thread; its own group.
@@ -464,39 +461,34 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
           // The features: 16-byte vectors quad * 4 .. + 3 of the tile's rows (tokens).
           const uint32_t src = smem_addr(&sm.tile[tC % NT][0]) + (quad >> 1) * kBlk;
 #pragma unroll 1
-          for (int k = 0; k < C::kStep / 16; ++k) {   // 16 tokens at a time
-            const int tok = grp * kHalf + step * C::kStep + 16 * k;
-            uint32_t r[2][4], t[TERMS][2][4];
+          for (int k = 0; k < C::kStep / 8; ++k) {   // 8 tokens at a time
+            const int tok = grp * kHalf + step * C::kStep + 8 * k;
+            uint32_t r[4], t[TERMS][4];
+            ldmatrix_x4_trans(src + (tok + (lane & 7)) * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) * 16), r);
+            const int pair = tok / 2 + (lane & 3);   // this lane's two tokens
+            const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
+            if (!whole) {   // rows past the chunk's tokens may hold anything
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const int at = tok + 8 * v + (lane & 7);
-              ldmatrix_x4_trans(src + at * 128 + ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) * 16), r[v]);
-              const int pair = (tok + 8 * v) / 2 + (lane & 3);   // this lane's two tokens
-              const float2 w = whole ? sm.w_full[pair] : sm.w_tail[pair];
-              if (!whole) {   // rows past the chunk's tokens may hold anything
+              for (int m = 0; m < 4; ++m)
+                r[m] = 2 * pair + 1 < tail ? r[m] : 2 * pair < tail ? r[m] & 0xffffu : 0u;
+            }
+            const uint64_t ww = f2_pack(w.x, w.y);
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                  r[v][m] = 2 * pair + 1 < tail ? r[v][m] : 2 * pair < tail ? r[v][m] & 0xffffu : 0u;
-              }
-              const uint64_t ww = f2_pack(w.x, w.y);
+            for (int m = 0; m < 4; ++m) {
+              uint64_t x = f2_mul(bf16x2_to_f2(r[m]), ww);
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                uint64_t x = f2_mul(bf16x2_to_f2(r[v][m]), ww);
-#pragma unroll
-                for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
-                  float x0, x1;
-                  f2_unpack(x, x0, x1);
-                  t[e][v][m] = pack_bf16x2(x0, x1);
-                  if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][v][m]));
-                }
+              for (int e = TERMS - 1; e >= 0; --e) {   // term 0 is the smallest
+                float x0, x1;
+                f2_unpack(x, x0, x1);
+                t[e][m] = pack_bf16x2(x0, x1);
+                if (e > 0) x = f2_sub(x, bf16x2_to_f2(t[e][m]));
               }
             }
-            const uint32_t dst = tCw + lane_off + (grp * C::kBufs + buf) * C::kBufCols + 8 * k;
+            const uint32_t dst = tCw + lane_off + (grp * C::kBufs + buf) * C::kBufCols + 4 * k;
 #pragma unroll
             for (int e = 0; e < TERMS; ++e) {
-              const uint32_t col = dst + e * (C::kStep / 2);
-              tmem_st_16x128b_x2(col, t[e][0][0], t[e][0][1], t[e][1][0], t[e][1][1]);
-              tmem_st_16x128b_x2(col + (16u << 16), t[e][0][2], t[e][0][3], t[e][1][2], t[e][1][3]);
+              tmem_st_16x128b(dst + e * (C::kStep / 2), t[e][0], t[e][1]);
+              tmem_st_16x128b(dst + e * (C::kStep / 2) + (16u << 16), t[e][2], t[e][3]);
             }
           }
           tmem_st_wait();
@@ -509,6 +501,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
         if (!(ok = wait(sm.kv_done, zi))) break;
         tc_fence_after();
         const float hi = cz.whole() ? hi_full : hi_tail, lo = cz.whole() ? lo_full : lo_tail;
+        const uint64_t hi2 = f2_pack(hi, hi), lo2 = f2_pack(lo, lo);
         cz.next(p);
         if (busy) {
 #pragma unroll
@@ -516,7 +509,11 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
             uint32_t t0[32];
             tmem_ld32(tbase + lane_off + col0 + q, t0);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) z[q + k] = fmaf(z[q + k], hi, fmaf(z[q + k], lo, __uint_as_float(t0[k])));
+            for (int k = 0; k < 32; k += 2) {
+              const uint64_t zz = f2_pack(z[q + k], z[q + k + 1]);
+              const uint64_t sum = f2_pack(__uint_as_float(t0[k]), __uint_as_float(t0[k + 1]));
+              f2_unpack(f2_fma(zz, hi2, f2_fma(zz, lo2, sum)), z[q + k], z[q + k + 1]);
+            }
           }
         }
         tc_fence_before();
@@ -641,12 +638,11 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
       tc_fence_after();
       const uint64_t wy = slow ? f2_pack(w, w) : f2_pack(1.f, 1.f);
 #pragma unroll 1
-      for (int q = 0; q < C::kBlocks; ++q) {
-        uint32_t y[64];
-        tmem_ld64(tY + lane_off + 64 * q, *reinterpret_cast<uint32_t(*)[32]>(y),
-                  *reinterpret_cast<uint32_t(*)[32]>(y + 32));
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t y[32];
+        tmem_ld32(tY + lane_off + 32 * q, y);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           uint32_t v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -655,8 +651,9 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
                       x1);
             v[e] = pack_bf16x2(x0, x1);
           }
-          if (staged) st_shared_v4(ydst + q * (4 * 32 * 128) + ((k ^ (lane & 7)) * 16), v);
-          else if (row < c.len) reinterpret_cast<uint4*>(dst)[8 * q + k] = make_uint4(v[0], v[1], v[2], v[3]);
+          const int vec = 4 * (q & 1) + k;
+          if (staged) st_shared_v4(ydst + (q >> 1) * (4 * 32 * 128) + ((vec ^ (lane & 7)) * 16), v);
+          else if (row < c.len) reinterpret_cast<uint4*>(dst)[4 * q + k] = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
       tc_fence_before();
