@@ -126,11 +126,37 @@ __device__ __forceinline__ void issue_qk(uint32_t tS, uint32_t q, uint32_t k) {
   }
 }
 template <int D, int KK0, int KK1>
-__device__ __forceinline__ void issue_av(uint32_t tO, uint32_t tP, uint32_t v, bool accumulate) {
+__device__ __forceinline__ void issue_av(uint32_t tO, uint32_t tS, uint32_t v, bool accumulate) {
   const uint64_t dv = smem_desc_sw128(v, kBlock, 1024);
 #pragma unroll
-  for (int kk = KK0; kk < KK1; ++kk)
-    umma_ts_elect(tO, tP + kk * 8, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), accumulate || kk > 0);
+  for (int kk = KK0; kk < KK1; ++kk) {
+    umma_ts_elect(tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), accumulate || kk > 0);
+    umma_ts_elect(tO, tS + 64 + kk * 8, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), 1u);
+  }
+}
+
+// softmax_chunk with P in two bf16 terms, e = high + low to 2^-17: a row that sees few keys
+// averages too few roundings of a single term. The high ones go to columns 64 .. 127 of the
+// scores, the low ones to 0 .. 63; all scores are in registers by then.
+__device__ __forceinline__ void softmax_chunk2(const float (&s)[kTile], int c, float sl2, float m_use, uint32_t tS,
+                                               float (&ls)[8]) {
+  uint32_t hi[16], lo[16];
+  const uint64_t sl2_2 = f2_pack(sl2, sl2);
+  const uint64_t nm_2 = f2_pack(-m_use, -m_use);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int col = c * 32 + 2 * j;
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(s[col], s[col + 1]), sl2_2, nm_2), x0, x1);
+    const float e0 = ex2_approx(x0);
+    const float e1 = ex2_approx(x1);
+    ls[j & 7] += e0 + e1;
+    hi[j] = pack_bf16x2(e0, e1);
+    f2_unpack(f2_sub(f2_pack(e0, e1), bf16x2_to_f2(hi[j])), x0, x1);
+    lo[j] = pack_bf16x2(x0, x1);
+  }
+  tmem_st16(tS + 64 + c * 16, hi);
+  tmem_st16(tS + c * 16, lo);
 }
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
@@ -191,6 +217,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
     tmem_alloc(smem_addr(&sm.tmem_base), 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may get ready
   if (warp == 9 && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
@@ -270,10 +297,10 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
         const uint32_t v = smem_addr(&sm.kv[vs][0]);
         if (!(ok = wait(sm.p_full[w][0], cnt[w]))) break;
         tc_fence_after();
-        issue_av<D, 0, 4>(tO[w], tS[w] + 64, v, i >= 2);
+        issue_av<D, 0, 4>(tO[w], tS[w], v, i >= 2);
         if (!(ok = wait(sm.p_full[w][1], cnt[w]))) break;
         tc_fence_after();
-        issue_av<D, 4, 8>(tO[w], tS[w] + 64, v, true);
+        issue_av<D, 4, 8>(tO[w], tS[w], v, true);
         ++cnt[w];
         if (i + 2 >= s.n) umma_commit_elect(smem_addr(&sm.o_done[w]));
         umma_commit_elect(smem_addr(&sm.kv_empty[vs]));
@@ -349,8 +376,8 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
           const float alpha = resc ? ex2_approx(m_prev - m_run) : 1.f;
           l_run *= alpha;
           float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          softmax_chunk(s, 0, sl2, m_use, tS, ls);
-          softmax_chunk(s, 1, sl2, m_use, tS, ls);
+          softmax_chunk2(s, 0, sl2, m_use, tS, ls);
+          softmax_chunk2(s, 1, sl2, m_use, tS, ls);
           if (i >= 2 && __any_sync(0xffffffffu, resc)) {
             // The accumulator holds the products before this tile, all complete.
 #pragma unroll
@@ -365,8 +392,8 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(smem_addr(&sm.p_full[wg][0]));
-          softmax_chunk(s, 2, sl2, m_use, tS, ls);
-          softmax_chunk(s, 3, sl2, m_use, tS, ls);
+          softmax_chunk2(s, 2, sl2, m_use, tS, ls);
+          softmax_chunk2(s, 3, sl2, m_use, tS, ls);
           l_run += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
           tmem_st_wait();
           tc_fence_before();
@@ -452,6 +479,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   __shared__ int warp_sum[8];
   tile_prefix<256>(p, before, warp_sum);
   __syncthreads();
+  // Launched while the attention kernel still runs: wait for its results.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = static_cast<int>(blockIdx.x) / row_blocks;
   const int row = (static_cast<int>(blockIdx.x) % row_blocks) * 8 + static_cast<int>(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -484,19 +513,43 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
     };
     const int c0 = holder(first), c1 = holder(last);
     if (c0 == c1) return;   // written whole
+    // Slot of CTA c's piece; null where the CTA has no run (fewer tiles than CTAs).
+    auto slot_of = [&](int c) -> const float* {
+      const int64_t f0 = total * c / p.n_cta;
+      if (f0 == total * (c + 1) / p.n_cta) return nullptr;
+      return p.parts + (2 * static_cast<int64_t>(c) + (f0 > first ? 0 : 1)) * (kTile * (D + 2));
+    };
+    // A lane per piece: the joint maximum and sum first, so that the sums' loads do not wait
+    // on one another.
     float M = -INFINITY, l = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      if (total * c / p.n_cta == total * (c + 1) / p.n_cta) continue;   // fewer tiles than CTAs: no run
-      const float* slot = p.parts + (2 * static_cast<int64_t>(c) + (total * c / p.n_cta > first ? 0 : 1)) * (kTile * (D + 2));
-      const float2 ml = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * row);
-      if (ml.x == -INFINITY) continue;
-      const float Mn = fmaxf(M, ml.x);
-      const float a = M == -INFINITY ? 0.f : ex2_approx(M - Mn), w = ex2_approx(ml.x - Mn);
-      M = Mn;
-      l = l * a + ml.y * w;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) acc[q] = acc[q] * a + slot[row * D + lane * kPer + q] * w;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float* slot = slot_of(c);
+      if (slot != nullptr) M = fmaxf(M, slot[kTile * D + 2 * row]);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int cb = c0; cb <= c1; cb += 32) {
+      const int c = cb + lane;
+      const float* slot = c <= c1 ? slot_of(c) : nullptr;
+      float w = 0.f;
+      if (slot != nullptr) {
+        const float2 ml = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * row);
+        if (ml.x != -INFINITY) w = ex2_approx(ml.x - M);
+        l = fmaf(ml.y, w, l);
+      }
+      const unsigned long long at = reinterpret_cast<unsigned long long>(w > 0.f ? slot : nullptr);
+      const int np = min(32, c1 - cb + 1);
+#pragma unroll 4
+      for (int k = 0; k < np; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, at, k));
+        if (from == nullptr) continue;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) acc[q] = fmaf(from[row * D + lane * kPer + q], wk, acc[q]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     inv = l > 0.f ? 1.f / l : 0.f;
     if (l > 0.f) lse = (M + __log2f(l)) * 0.69314718055994531f;
   }
@@ -520,8 +573,16 @@ bool launch_cache(const CacheLaunch& L, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return false;
   const int rows = L.p.tok_per_tile * L.p.G;
   const int row_blocks = (rows + 7) / 8;
-  cache_join_kernel<D><<<L.p.B * L.p.Hkv * L.p.row_tiles * row_blocks, 256, 0, stream>>>(L.p, row_blocks);
-  return cudaGetLastError() == cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L.p.B * L.p.Hkv * L.p.row_tiles * row_blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, L.p, row_blocks) == cudaSuccess;
 }
 
 }  // namespace
