@@ -27,9 +27,10 @@
 #include "geometry.h"
 #include "plan_view.h"
 #include "sm100.cuh"
-#include "softmax.cuh"
 
 namespace cpattn {
+
+using namespace sm100;
 
 namespace {
 
@@ -106,9 +107,9 @@ __device__ __forceinline__ CacheSeg seg_at(const CacheParams& p, const int* befo
   CacheSeg s;
   s.b = lo;
   s.nt = before[lo + 1] - before[lo];
-  const int64_t rem = f - static_cast<int64_t>(before[lo]) * hr;
-  const int u = static_cast<int>(rem / s.nt);
-  s.t0 = static_cast<int>(rem - static_cast<int64_t>(u) * s.nt);
+  const int rem = static_cast<int>(f - static_cast<int64_t>(before[lo]) * hr);   // the plan keeps tiles in int32
+  const int u = rem / s.nt;
+  s.t0 = rem - u * s.nt;
   s.hk = u / p.row_tiles;
   s.rt = u - s.hk * p.row_tiles;
   const int64_t left = end - f;
@@ -125,43 +126,29 @@ __device__ __forceinline__ void issue_qk(uint32_t tS, uint32_t q, uint32_t k) {
     umma_ss_elect(tS, dq + off, dk + off, kIdescQK, kk > 0);
   }
 }
+// O (+)= P V over keys [16 KK0, 16 KK1): P is two bf16 terms, 32 columns of a score tile
+// holding the high ones of their 32 keys, then the low ones.
 template <int D, int KK0, int KK1>
 __device__ __forceinline__ void issue_av(uint32_t tO, uint32_t tS, uint32_t v, bool accumulate) {
   const uint64_t dv = smem_desc_sw128(v, kBlock, 1024);
 #pragma unroll
   for (int kk = KK0; kk < KK1; ++kk) {
-    umma_ts_elect(tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), accumulate || kk > 0);
-    umma_ts_elect(tO, tS + 64 + kk * 8, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), 1u);
+    const uint32_t tP = tS + (kk >> 1) * 32 + (kk & 1) * 8;
+    umma_ts_elect(tO, tP, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), accumulate || kk > 0);
+    umma_ts_elect(tO, tP + 16, dv + ((kk * 2048) >> 4), idesc_bf16_f32(128, D, 0, 1), 1u);
   }
-}
-
-// softmax_chunk with P in two bf16 terms, e = high + low to 2^-17: a row that sees few keys
-// averages too few roundings of a single term. The high ones go to columns 64 .. 127 of the
-// scores, the low ones to 0 .. 63; all scores are in registers by then.
-__device__ __forceinline__ void softmax_chunk2(const float (&s)[kTile], int c, float sl2, float m_use, uint32_t tS,
-                                               float (&ls)[8]) {
-  uint32_t hi[16], lo[16];
-  const uint64_t sl2_2 = f2_pack(sl2, sl2);
-  const uint64_t nm_2 = f2_pack(-m_use, -m_use);
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const int col = c * 32 + 2 * j;
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(s[col], s[col + 1]), sl2_2, nm_2), x0, x1);
-    const float e0 = ex2_approx(x0);
-    const float e1 = ex2_approx(x1);
-    ls[j & 7] += e0 + e1;
-    hi[j] = pack_bf16x2(e0, e1);
-    f2_unpack(f2_sub(f2_pack(e0, e1), bf16x2_to_f2(hi[j])), x0, x1);
-    lo[j] = pack_bf16x2(x0, x1);
-  }
-  tmem_st16(tS + 64 + c * 16, hi);
-  tmem_st16(tS + c * 16, lo);
 }
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
-__device__ __forceinline__ uint64_t shifted(uint64_t w, int s) {
-  return s >= 64 || s <= -64 ? 0ull : s >= 0 ? w << s : w >> -s;
+// Which of 32 columns a row sees: those before `lim` (cached keys), and from there on those
+// of the drafted tokens' word.
+__device__ __forceinline__ uint32_t keep_bits(uint64_t word, int lim) {
+  const uint64_t tree = lim >= 32 || lim <= -64 ? 0ull : lim >= 0 ? word << lim : word >> -lim;
+  return static_cast<uint32_t>(low_bits(lim) | tree);
+}
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], uint32_t keep) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) s[j] = keep >> j & 1u ? s[j] : 0xff800000u;   // -inf
 }
 
 // Row r of the query tile: which token and query head, and where its results go.
@@ -237,17 +224,22 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
     // ---------------------------------------------------------------- TMA
     const uint64_t pol = l2_policy_evict_first();
     bool ok = true;
-    int kv = 0, unit = 0;
+    int kv = 0, unit = 0, q_loads = 0;
     for (int64_t f = f0; f < f1 && ok; ++unit) {
       const CacheSeg s = seg_at(p, sm.before, f, f1);
       f += s.n;
-      if (unit > 0 && !(ok = wait(sm.q_empty, unit - 1))) break;
-      mbar_arrive_expect_tx_elect(smem_addr(&sm.q_full), C::kBlocks * p.G * p.tok_per_tile * 128);
-      for (int blk = 0; blk < C::kBlocks; ++blk)
-        tma_load_4d_elect(smem_addr(&sm.q[0]) + blk * kBlock, &tm_q, smem_addr(&sm.q_full), blk * 64, s.hk * p.G,
-                          s.rt * p.tok_per_tile, s.b, pol);
-      // K(0), K(1), then V(i), K(i + 2): the order the products take them.
+      // K(0), K(1), then V(i), K(i + 2): the order the products take them. The first of a unit
+      // are loaded before its Q, which waits for the unit before to have read its own.
+      bool q_loaded = false;
       for (int j = 0; j < 2 * s.n; ++j, ++kv) {
+        if (j == (s.n == 1 ? 1 : 2)) {
+          if (unit > 0 && !(ok = wait(sm.q_empty, unit - 1))) break;
+          q_loaded = true;
+          mbar_arrive_expect_tx_elect(smem_addr(&sm.q_full), C::kBlocks * p.G * p.tok_per_tile * 128);
+          for (int blk = 0; blk < C::kBlocks; ++blk)
+            tma_load_4d_elect(smem_addr(&sm.q[0]) + blk * kBlock, &tm_q, smem_addr(&sm.q_full), blk * 64, s.hk * p.G,
+                              s.rt * p.tok_per_tile, s.b, pol);
+        }
         const int key = j == 0 ? 0 : s.n == 1 ? -1 : j == 1 ? 1 : (j & 1) && (j + 1) / 2 < s.n ? (j + 1) / 2 : -1;
         const int tile = key >= 0 ? key : j == 2 * s.n - 1 ? s.n - 1 : (j - 2) / 2;
         const int st = kv % NS;
@@ -257,11 +249,12 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
           tma_load_4d_elect(smem_addr(&sm.kv[st][0]) + blk * kBlock, key >= 0 ? &tm_k : &tm_v,
                             smem_addr(&sm.kv_full[st]), blk * 64, s.hk, (s.t0 + tile) * kTile, s.b, pol);
       }
+      q_loads += q_loaded;
     }
     if (!ok) {   // abort: let every load this warp issued land before the CTA exits
       for (int k = kv - NS; k < kv; ++k)
         if (k >= 0) mbar_wait_drain(smem_addr(&sm.kv_full[k % NS]), (k / NS) & 1, p.wait_limit_ns);
-      if (unit > 0) mbar_wait_drain(smem_addr(&sm.q_full), (unit - 1) & 1, p.wait_limit_ns);
+      if (q_loads > 0) mbar_wait_drain(smem_addr(&sm.q_full), (q_loads - 1) & 1, p.wait_limit_ns);
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA
@@ -280,6 +273,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
         issue_qk<D>(tS[i], q, smem_addr(&sm.kv[st][0]));
         umma_commit_elect(smem_addr(&sm.s_full[i]));
         umma_commit_elect(smem_addr(&sm.kv_empty[st]));
+        if (i + 1 == s.n) umma_commit_elect(smem_addr(&sm.q_empty));
         issued = true;
       }
       for (int i = 0; i < s.n && ok; ++i) {
@@ -308,10 +302,9 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
           issue_qk<D>(tS[w], q, smem_addr(&sm.kv[ks][0]));
           umma_commit_elect(smem_addr(&sm.s_full[w]));
           umma_commit_elect(smem_addr(&sm.kv_empty[ks]));
+          if (i + 3 == s.n) umma_commit_elect(smem_addr(&sm.q_empty));   // the unit's last scores
         }
       }
-      if (!ok) break;
-      umma_commit_elect(smem_addr(&sm.q_empty));
     }
     if (issued) {   // every product and commit has to finish before TMEM is freed
       umma_commit_elect(smem_addr(&sm.drain));
@@ -358,29 +351,29 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         if (busy) {
-          float s[kTile];
-          tmem_ld128(tS, reinterpret_cast<uint32_t*>(s));
-          const bool masked = k0 + kTile > len;
-          const int lim = len - k0;
-          const uint64_t keep0 = low_bits(lim) | shifted(word, lim), keep1 = low_bits(lim - 64) | shifted(word, lim - 64);
-          if (masked) {
+          // Two walks over the row's scores, 32 columns at a time from TMEM: the maximum, then
+          // the exponentials, P written over the columns just read. (Holding all 128 scores
+          // needs the registers of both and straight-line code that outruns the instruction cache.)
+          const int lim = len - k0;   // columns below it are cached keys
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tmem_ld32(tS + 32 * c, s);
+            if (lim < kTile) mask_scores(s, keep_bits(word, lim - 32 * c));
 #pragma unroll
-            for (int j = 0; j < kTile; ++j) s[j] = ((j < 64 ? keep0 : keep1) >> (j & 63)) & 1 ? s[j] : -INFINITY;
+            for (int j = 0; j < 32; j += 2) mt = max3(mt, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
           }
           // Online softmax with a lazily moved maximum, as in attn_fwd.cu.
           const float m_prev = m_run;
-          const float mt = fmaxf(half_max(s, 0), half_max(s, 2)) * sl2;
-          const bool resc = mt - m_run > kCacheRescale;   // false while both are -inf
-          if (resc) m_run = mt;
+          const bool resc = mt * sl2 - m_run > kCacheRescale;   // false while both are -inf
+          if (resc) m_run = mt * sl2;
           const float m_use = m_run == -INFINITY ? 0.f : m_run;
           const float alpha = resc ? ex2_approx(m_prev - m_run) : 1.f;
           l_run *= alpha;
-          float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          softmax_chunk2(s, 0, sl2, m_use, tS, ls);
-          softmax_chunk2(s, 1, sl2, m_use, tS, ls);
           if (i >= 2 && __any_sync(0xffffffffu, resc)) {
             // The accumulator holds the products before this tile, all complete.
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t o[16];
               tmem_ld16(tO + c, o);
@@ -389,15 +382,33 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
               tmem_st16(tO + c, o);
             }
           }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(smem_addr(&sm.p_full[wg][0]));
-          softmax_chunk2(s, 2, sl2, m_use, tS, ls);
-          softmax_chunk2(s, 3, sl2, m_use, tS, ls);
-          l_run += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(smem_addr(&sm.p_full[wg][1]));
+          const uint64_t sl2_2 = f2_pack(sl2, sl2), nm_2 = f2_pack(-m_use, -m_use);
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32], hi[16], lo[16];
+            tmem_ld32(tS + 32 * c, s);
+            if (lim < kTile) mask_scores(s, keep_bits(word, lim - 32 * c));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sl2_2, nm_2), x0, x1);
+              const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+              l0 += e0;
+              l1 += e1;
+              hi[j] = pack_bf16x2(e0, e1);
+              f2_unpack(f2_sub(f2_pack(e0, e1), bf16x2_to_f2(hi[j])), x0, x1);
+              lo[j] = pack_bf16x2(x0, x1);
+            }
+            tmem_st16(tS + 32 * c, hi);
+            tmem_st16(tS + 32 * c + 16, lo);
+            if (c & 1) {   // half the keys: their part of P V may start
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(smem_addr(&sm.p_full[wg][c >> 1]));
+            }
+          }
+          l_run += l0 + l1;
         } else {
           mbar_arrive(smem_addr(&sm.p_full[wg][0]));
           mbar_arrive(smem_addr(&sm.p_full[wg][1]));
@@ -666,12 +677,11 @@ int cp_cache_plan(cp_cache_plan_t* out, int B, int Hq, int Hkv, int D, int capac
   if (D != 64 && D != 128) return CP_ERR_UNSUPPORTED;
   if (Hq % Hkv != 0 || Hq / Hkv > kTile || T > kCacheMaxT || B > kCacheMaxB) return CP_ERR_UNSUPPORTED;
   // Tile counts, row blocks of the join and cache rows are int32.
+  if (capacity > (1 << 30) || Hq > (1 << 20)) return CP_ERR_UNSUPPORTED;
   const int64_t tiles = (static_cast<int64_t>(capacity) + kTile - 1) / kTile;
-  if (capacity > (1 << 30) || tiles * B > INT32_MAX || static_cast<int64_t>(B) * Hkv > (1 << 24) || Hq > (1 << 20))
-    return CP_ERR_UNSUPPORTED;
   const int64_t per_tile = kTile / (Hq / Hkv);
-  if (static_cast<int64_t>(B) * Hkv * ((T + per_tile - 1) / per_tile) * (kTile / 8) > INT32_MAX)
-    return CP_ERR_UNSUPPORTED;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * ((T + per_tile - 1) / per_tile);
+  if (units * (kTile / 8) > INT32_MAX || units * tiles > INT32_MAX) return CP_ERR_UNSUPPORTED;
   cp_cache_plan_s* c = new (std::nothrow) cp_cache_plan_s;
   if (c == nullptr) return CP_ERR_CUDA;
   c->B = B;
