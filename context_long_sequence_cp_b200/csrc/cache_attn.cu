@@ -53,8 +53,8 @@ struct alignas(1024) CacheSmem {
   uint64_t kv_full[CacheCfg<D>::kStages], kv_empty[CacheCfg<D>::kStages];
   uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_done[2], ml_ready, unit_done, drain;
   float2 ml[2][kTile];               // (max, sum) of each warpgroup's rows
-  int before[kCacheMaxB + 1];        // key tiles of the sequences before b
-  int warp_sum[kCacheThreads / 32];
+  int2 before[kCacheMaxB + 1];       // see CacheSpan
+  int2 warp_sum[kCacheThreads / 32];
   uint32_t tmem_base;
   WaitBlock wblk;
 };
@@ -67,53 +67,93 @@ __device__ __forceinline__ int key_count(const CacheParams& p, int b) {
   return len < 0 || len > p.cap - extra ? -1 : len + extra;
 }
 
-// Prefix sums of the sequences' key tiles, by all threads of the block.
+// The work of all units, laid end to end in slots and cut into equal runs, one per CTA: a
+// unit's key tiles, after kUnitSlots empty slots that stand for its start and end (queries
+// loaded, accumulators joined and written: about two tiles' time), where there are tiles
+// enough for the balance to matter.
+constexpr int kUnitSlots = 2;
+struct CacheSpan {
+  const int2* before;   // key tiles of the sequences before b, and those of them that have keys
+  int units;            // units of a sequence
+  int extra;            // empty slots per unit
+  int per, more;        // CTA c holds `per` slots, and one more where c < more
+  __device__ __forceinline__ int start(int c) const { return c * per + min(c, more); }
+  __device__ __forceinline__ int holder(int f) const {   // the CTA that holds slot f
+    const int wide = more * (per + 1);
+    return f < wide ? f / (per + 1) : more + (f - wide) / per;
+  }
+  __device__ __forceinline__ int slots_before(int b) const { return (before[b].x + extra * before[b].y) * units; }
+  __device__ __forceinline__ int tiles(int b) const { return before[b + 1].x - before[b].x; }
+};
+
+// Fills before[0 .. B], by all threads of the block.
 template <int THREADS>
-__device__ __forceinline__ void tile_prefix(const CacheParams& p, int* before, int* warp_sum) {
-  int carry = 0;
-  if (threadIdx.x == 0) before[0] = 0;
+__device__ __forceinline__ CacheSpan cache_span(const CacheParams& p, int2* before, int2* warp_sum) {
+  int2 carry = make_int2(0, 0);
+  if (threadIdx.x == 0) before[0] = carry;
   for (int b0 = 0; b0 < p.B; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    int v = b < p.B ? (max(key_count(p, b), 0) + kTile - 1) / kTile : 0;
+    int2 v = make_int2(b < p.B ? (max(key_count(p, b), 0) + kTile - 1) / kTile : 0, 0);
+    v.y = v.x > 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if ((threadIdx.x & 31) >= o) v += u;
+      const int ux = __shfl_up_sync(0xffffffffu, v.x, o), uy = __shfl_up_sync(0xffffffffu, v.y, o);
+      if ((threadIdx.x & 31) >= o) {
+        v.x += ux;
+        v.y += uy;
+      }
     }
     if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = v;
     __syncthreads();
-    int base = carry;
-    for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) base += warp_sum[w];
-    if (b < p.B) before[b + 1] = base + v;
-    for (int w = 0; w < THREADS / 32; ++w) carry += warp_sum[w];
+    v.x += carry.x;
+    v.y += carry.y;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < static_cast<int>(threadIdx.x >> 5)) {
+        v.x += warp_sum[w].x;
+        v.y += warp_sum[w].y;
+      }
+      carry.x += warp_sum[w].x;
+      carry.y += warp_sum[w].y;
+    }
+    if (b < p.B) before[b + 1] = v;
     __syncthreads();
   }
+  CacheSpan s;
+  s.before = before;
+  s.units = p.Hkv * p.row_tiles;
+  s.extra = static_cast<int64_t>(carry.x) * s.units >= 4 * p.n_cta ? kUnitSlots : 0;
+  const int total = (carry.x + carry.y * s.extra) * s.units;   // the plan keeps it in int32
+  s.per = total / p.n_cta;
+  s.more = total - s.per * p.n_cta;
+  return s;
 }
 
-// A run of key tiles of one unit (sequence b, key/value head hk, query tile rt).
+// A run of key tiles of one unit (sequence b, key/value head hk, query tile rt); n may be
+// 0 where the piece holds empty slots only.
 struct CacheSeg {
   int b, hk, rt;
   int t0, n, nt;   // key tiles [t0, t0 + n) of nt
+  int next;        // slot after the piece
 };
-// The piece of the flattened tiles that starts at f and ends at `end` at most.
-__device__ __forceinline__ CacheSeg seg_at(const CacheParams& p, const int* before, int64_t f, int64_t end) {
-  const int hr = p.Hkv * p.row_tiles;
-  int lo = 0, hi = p.B - 1;   // last b with before[b] * hr <= f: never an empty sequence
+// The piece of the slots that starts at f and ends at `end` at most.
+__device__ __forceinline__ CacheSeg seg_at(const CacheParams& p, const CacheSpan& sp, int f, int end) {
+  int lo = 0, hi = p.B - 1;   // last b that starts at f or before: never a sequence without keys
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(before[mid]) * hr <= f) lo = mid;
+    if (sp.slots_before(mid) <= f) lo = mid;
     else hi = mid - 1;
   }
   CacheSeg s;
   s.b = lo;
-  s.nt = before[lo + 1] - before[lo];
-  const int rem = static_cast<int>(f - static_cast<int64_t>(before[lo]) * hr);   // the plan keeps tiles in int32
-  const int u = rem / s.nt;
-  s.t0 = rem - u * s.nt;
+  s.nt = sp.tiles(lo);
+  const int rem = f - sp.slots_before(lo), len = s.nt + sp.extra;
+  const int u = rem / len, pos = rem - u * len;
   s.hk = u / p.row_tiles;
   s.rt = u - s.hk * p.row_tiles;
-  const int64_t left = end - f;
-  s.n = static_cast<int>(left < s.nt - s.t0 ? left : s.nt - s.t0);
+  const int stop = min(pos + end - f, len);
+  s.next = f + stop - pos;
+  s.t0 = max(pos - sp.extra, 0);
+  s.n = max(stop - sp.extra, 0) - s.t0;
   return s;
 }
 
@@ -210,14 +250,13 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  tile_prefix<kCacheThreads>(p, sm.before, sm.warp_sum);
+  const CacheSpan span = cache_span<kCacheThreads>(p, sm.before, sm.warp_sum);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl ctl = wait_ctl(sm.wblk);
-  const int64_t total = static_cast<int64_t>(sm.before[p.B]) * p.Hkv * p.row_tiles;
-  const int64_t f0 = total * blockIdx.x / p.n_cta, f1 = total * (blockIdx.x + 1) / p.n_cta;
+  const int f0 = span.start(static_cast<int>(blockIdx.x)), f1 = span.start(static_cast<int>(blockIdx.x) + 1);
   auto wait = [&](uint64_t& bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(smem_addr(&bar), phase & 1, ctl)); };
 
   if (warp == 9) {
@@ -225,9 +264,10 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
     const uint64_t pol = l2_policy_evict_first();
     bool ok = true;
     int kv = 0, unit = 0, q_loads = 0;
-    for (int64_t f = f0; f < f1 && ok; ++unit) {
-      const CacheSeg s = seg_at(p, sm.before, f, f1);
-      f += s.n;
+    for (int f = f0; f < f1 && ok;) {
+      const CacheSeg s = seg_at(p, span, f, f1);
+      f = s.next;
+      if (s.n == 0) continue;
       // K(0), K(1), then V(i), K(i + 2): the order the products take them. The first of a unit
       // are loaded before its Q, which waits for the unit before to have read its own.
       bool q_loaded = false;
@@ -250,6 +290,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
                             smem_addr(&sm.kv_full[st]), blk * 64, s.hk, (s.t0 + tile) * kTile, s.b, pol);
       }
       q_loads += q_loaded;
+      ++unit;
     }
     if (!ok) {   // abort: let every load this warp issued land before the CTA exits
       for (int k = kv - NS; k < kv; ++k)
@@ -262,9 +303,10 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
     const uint32_t tS[2] = {tbase, tbase + 128}, tO[2] = {tbase + 256, tbase + 256 + D};
     bool ok = true, issued = false;
     int kv = 0, unit = 0, cnt[2] = {0, 0};
-    for (int64_t f = f0; f < f1 && ok; ++unit) {
-      const CacheSeg s = seg_at(p, sm.before, f, f1);
-      f += s.n;
+    for (int f = f0; f < f1 && ok;) {
+      const CacheSeg s = seg_at(p, span, f, f1);
+      f = s.next;
+      if (s.n == 0) continue;
       if (!(ok = wait(sm.q_full, unit))) break;
       for (int i = 0; i < 2 && i < s.n; ++i, ++kv) {
         const int st = kv % NS;
@@ -305,6 +347,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
           if (i + 3 == s.n) umma_commit_elect(smem_addr(&sm.q_empty));   // the unit's last scores
         }
       }
+      ++unit;
     }
     if (issued) {   // every product and commit has to finish before TMEM is freed
       umma_commit_elect(smem_addr(&sm.drain));
@@ -320,9 +363,10 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
     const float sl2 = p.scale_log2;
     bool ok = true;
     int kv = 0, unit = 0, s_cnt = 0, od_cnt = 0;
-    for (int64_t f = f0; f < f1 && ok; ++unit) {
-      const CacheSeg sg = seg_at(p, sm.before, f, f1);
-      f += sg.n;
+    for (int f = f0; f < f1 && ok;) {
+      const CacheSeg sg = seg_at(p, span, f, f1);
+      f = sg.next;
+      if (sg.n == 0) continue;
       const CacheRow cr = cache_row(p, sg.hk, sg.rt, row);
       const bool busy = __any_sync(0xffffffffu, cr.valid);   // a warp without rows only keeps the barriers' pace
       const int len = __ldg(p.lengths + sg.b), keys = len + (p.own ? p.T : 0);
@@ -470,6 +514,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
       }
       tc_fence_before();
       mbar_arrive(smem_addr(&sm.unit_done));
+      ++unit;
     }
   }
 
@@ -486,20 +531,19 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
 // cache (NaN).
 template <int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheParams p, int row_blocks) {
-  __shared__ int before[kCacheMaxB + 1];
-  __shared__ int warp_sum[8];
-  tile_prefix<256>(p, before, warp_sum);
+  __shared__ int2 before[kCacheMaxB + 1];
+  __shared__ int2 warp_sum[8];
+  const CacheSpan span = cache_span<256>(p, before, warp_sum);
   __syncthreads();
   // Launched while the attention kernel still runs: wait for its results.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = static_cast<int>(blockIdx.x) / row_blocks;
   const int row = (static_cast<int>(blockIdx.x) % row_blocks) * 8 + static_cast<int>(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int hr = p.Hkv * p.row_tiles;
-  const int b = unit / hr, u = unit - b * hr;
+  const int b = unit / span.units, u = unit - b * span.units;
   const CacheRow cr = cache_row(p, u / p.row_tiles, u % p.row_tiles, row);
   if (row >= kTile || !cr.valid) return;
-  const int nt = before[b + 1] - before[b];
+  const int nt = span.tiles(b);
   constexpr int kPer = D / 32;
   float acc[kPer];
 #pragma unroll
@@ -513,29 +557,18 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
       inv = 1.f;
     }
   } else {
-    const int64_t total = static_cast<int64_t>(before[p.B]) * hr;
-    const int64_t first = static_cast<int64_t>(before[b]) * hr + static_cast<int64_t>(u) * nt, last = first + nt - 1;
-    // CTA c holds tiles [total c / n, total (c + 1) / n): the last c whose start is <= f holds f.
-    auto holder = [&](int64_t f) {
-      int64_t c = (f * p.n_cta) / total;
-      while (total * (c + 1) / p.n_cta <= f) ++c;
-      while (total * c / p.n_cta > f) --c;
-      return static_cast<int>(c);
-    };
-    const int c0 = holder(first), c1 = holder(last);
+    const int first = span.slots_before(b) + u * (nt + span.extra) + span.extra;   // slot of the first tile
+    const int c0 = span.holder(first), c1 = span.holder(first + nt - 1);
     if (c0 == c1) return;   // written whole
-    // Slot of CTA c's piece; null where the CTA has no run (fewer tiles than CTAs).
-    auto slot_of = [&](int c) -> const float* {
-      const int64_t f0 = total * c / p.n_cta;
-      if (f0 == total * (c + 1) / p.n_cta) return nullptr;
-      return p.parts + (2 * static_cast<int64_t>(c) + (f0 > first ? 0 : 1)) * (kTile * (D + 2));
+    // A piece that starts inside the unit lies in its CTA's first slot, else in the second.
+    auto slot_of = [&](int c) {
+      return p.parts + (2 * static_cast<int64_t>(c) + (span.start(c) > first ? 0 : 1)) * (kTile * (D + 2));
     };
     // A lane per piece: the joint maximum and sum first, so that the sums' loads do not wait
     // on one another.
     float M = -INFINITY, l = 0.f;
     for (int c = c0 + lane; c <= c1; c += 32) {
-      const float* slot = slot_of(c);
-      if (slot != nullptr) M = fmaxf(M, slot[kTile * D + 2 * row]);
+      M = fmaxf(M, slot_of(c)[kTile * D + 2 * row]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -681,7 +714,7 @@ int cp_cache_plan(cp_cache_plan_t* out, int B, int Hq, int Hkv, int D, int capac
   const int64_t tiles = (static_cast<int64_t>(capacity) + kTile - 1) / kTile;
   const int64_t per_tile = kTile / (Hq / Hkv);
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((T + per_tile - 1) / per_tile);
-  if (units * (kTile / 8) > INT32_MAX || units * tiles > INT32_MAX) return CP_ERR_UNSUPPORTED;
+  if (units * (kTile / 8) > INT32_MAX || units * (tiles + kUnitSlots) > INT32_MAX) return CP_ERR_UNSUPPORTED;
   cp_cache_plan_s* c = new (std::nothrow) cp_cache_plan_s;
   if (c == nullptr) return CP_ERR_CUDA;
   c->B = B;
