@@ -443,10 +443,11 @@ def _enqueue(device, stream, body):
     if device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {device}")
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return body(torch.cuda.current_stream().cuda_stream)
+        # The raw queries: a small call is launch-bound, and the Stream object alone costs 4 us.
+        if device.index == torch._C._cuda_getDevice():
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
         with torch.cuda.device(device):
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.device(device), torch.cuda.stream(stream):

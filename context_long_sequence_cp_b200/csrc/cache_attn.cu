@@ -210,6 +210,12 @@ __device__ __forceinline__ void store_lse(const CacheParams& p, int b, const Cac
   else p.lse[(static_cast<int64_t>(b) * p.Hq + c.hq) * p.T + c.t] = lse;
 }
 
+// 1 / sum and lse of a row; a row that sees nothing gets 0 and -inf, a NaN stays one.
+__device__ __forceinline__ float inv_sum(float l) { return l > 0.f ? 1.f / l : l == 0.f ? 0.f : l; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : l == 0.f ? -INFINITY : l;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kCacheThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
       const bool whole = sg.n == sg.nt;
       // A unit cut at this CTA's start goes to its first slot, one cut at its end to the second.
       float* slot = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (sg.t0 > 0 ? 0 : 1)) * (kTile * (D + 2));
-      const float inv = whole && l > 0.f ? 1.f / l : (whole ? 0.f : 1.f);
+      const float inv = whole ? inv_sum(l) : 1.f;
       const int64_t out = (static_cast<int64_t>(sg.b) * p.T + cr.t) * p.Hq + cr.hq;
       if (busy) {
 #pragma unroll
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
         }
       }
       if (wg == 0 && cr.valid) {
-        if (whole) store_lse(p, sg.b, cr, l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY);
+        if (whole) store_lse(p, sg.b, cr, row_lse(M, l));
         else *reinterpret_cast<float2*>(slot + kTile * D + 2 * row) = make_float2(M, l);
       }
       tc_fence_before();
@@ -544,7 +550,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   const CacheRow cr = cache_row(p, u / p.row_tiles, u % p.row_tiles, row);
   if (row >= kTile || !cr.valid) return;
   const int nt = span.tiles(b);
-  constexpr int kPer = D / 32;
+  constexpr int kPer = D / 16;   // columns of a lane: half a warp spans the row, the halves take every other piece
+  const int half = lane >> 4, col = (lane & 15) * kPer;
   float acc[kPer];
 #pragma unroll
   for (int q = 0; q < kPer; ++q) acc[q] = 0.f;
@@ -567,9 +574,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
     // A lane per piece: the joint maximum and sum first, so that the sums' loads do not wait
     // on one another.
     float M = -INFINITY, l = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      M = fmaxf(M, slot_of(c)[kTile * D + 2 * row]);
-    }
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot_of(c)[kTile * D + 2 * row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     for (int cb = c0; cb <= c1; cb += 32) {
@@ -578,31 +583,42 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
       float w = 0.f;
       if (slot != nullptr) {
         const float2 ml = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * row);
-        if (ml.x != -INFINITY) w = ex2_approx(ml.x - M);
+        w = ml.x == -INFINITY ? ml.y : ex2_approx(ml.x - M);   // a sum without a maximum is 0 or NaN
         l = fmaf(ml.y, w, l);
       }
-      const unsigned long long at = reinterpret_cast<unsigned long long>(w > 0.f ? slot : nullptr);
       const int np = min(32, c1 - cb + 1);
 #pragma unroll 4
-      for (int k = 0; k < np; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, at, k));
-        if (from == nullptr) continue;
+      for (int k = 0; k < np; k += 2) {
+        const float wk = __shfl_sync(0xffffffffu, w, k + half);   // 0 past the last piece
+        if (wk == 0.f) continue;                                  // its rows may hold anything
+        const float4* from = reinterpret_cast<const float4*>(slot_of(cb + k + half) + row * D + col);
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) acc[q] = fmaf(from[row * D + lane * kPer + q], wk, acc[q]);
+        for (int q = 0; q < kPer / 4; ++q) {
+          const float4 v = from[q];
+          acc[4 * q] = fmaf(v.x, wk, acc[4 * q]);
+          acc[4 * q + 1] = fmaf(v.y, wk, acc[4 * q + 1]);
+          acc[4 * q + 2] = fmaf(v.z, wk, acc[4 * q + 2]);
+          acc[4 * q + 3] = fmaf(v.w, wk, acc[4 * q + 3]);
+        }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    inv = l > 0.f ? 1.f / l : 0.f;
-    if (l > 0.f) lse = (M + __log2f(l)) * 0.69314718055994531f;
-  }
-  const int64_t out = ((static_cast<int64_t>(b) * p.T + cr.t) * p.Hq + cr.hq) * D + lane * kPer;
+    for (int q = 0; q < kPer; ++q) acc[q] += __shfl_xor_sync(0xffffffffu, acc[q], 16);
 #pragma unroll
-  for (int q = 0; q < kPer; q += 2) {
-    const float x = acc[q] * inv, y = acc[q + 1] * inv;
-    if (p.o_part != nullptr) *reinterpret_cast<float2*>(p.o_part + out + q) = make_float2(x, y);
-    else *reinterpret_cast<uint32_t*>(p.o + out + q) = pack_bf16x2(x, y);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    inv = inv_sum(l);
+    lse = row_lse(M, l);
+  }
+  const int64_t out = ((static_cast<int64_t>(b) * p.T + cr.t) * p.Hq + cr.hq) * D + col;
+  if (half == 0) {
+#pragma unroll
+    for (int q = 0; q < kPer; q += 4) {
+      const float y[4] = {acc[q] * inv, acc[q + 1] * inv, acc[q + 2] * inv, acc[q + 3] * inv};
+      if (p.o_part != nullptr)
+        *reinterpret_cast<float4*>(p.o_part + out + q) = make_float4(y[0], y[1], y[2], y[3]);
+      else
+        *reinterpret_cast<uint2*>(p.o + out + q) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    }
   }
   if (lane == 0) store_lse(p, b, cr, lse);
 }
