@@ -487,11 +487,9 @@ PermuteArgs permute_args(const cp_attn_plan_s* p, int direction, int elem_bytes)
 namespace cpattn {
 
 int plan_view(const cp_attn_plan_s* plan, PlanView* out) {
-  const int rc = on_plan_device(plan);
-  if (rc != CP_OK) return rc;
   *out = PlanView{plan->B,      plan->H,     plan->S,   plan->D,       plan->N, plan->causal,
                   plan->layout, plan->scale, plan->sms, plan->d_status};
-  return CP_OK;
+  return on_plan_device(plan);
 }
 
 bool encode_map_4d(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t d3, int box1,

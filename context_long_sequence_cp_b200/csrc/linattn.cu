@@ -867,11 +867,10 @@ bool make_scan(LinScan* L, const PlanView& v, const ScanCall& s, const float* lo
 // Arguments common to the forward and the backward.
 int check_plan(cp_attn_plan_t plan, PlanView* v) {
   const int rc = plan_view(plan, v);
-  if (rc != CP_OK) return rc;
   if (v->layout == CP_LAYOUT_ULYSSES || !v->causal) return CP_ERR_UNSUPPORTED;
   // one CTA per scan, (batch, head) and segment, indexed in int32
   if (static_cast<int64_t>(v->B) * v->H > (int64_t(1) << 29) / kMaxSegments) return CP_ERR_UNSUPPORTED;
-  return CP_OK;
+  return rc;
 }
 
 }  // namespace

@@ -22,8 +22,8 @@ struct PlanView {
   int* status;   // device status word
 };
 
-// Fills *out; CP_ERR_CUDA when the plan was made without a device,
-// CP_ERR_INVALID_ARG when another device than the plan's is current.
+// Fills *out. Returns CP_ERR_CUDA when the plan was made without a device,
+// CP_ERR_INVALID_ARG when another device than the plan's is current, else CP_OK.
 int plan_view(const cp_attn_plan_s* plan, PlanView* out);
 
 // Bytes are 16-byte aligned.

@@ -21,10 +21,15 @@ Contents:
     chain rule on the forward's definition.
   * ``sp_norm``    — reduce-scatter / all-gather over virtual ranks and the
     LayerNorm + dropout + residual step on sequence shards.
+  * ``rope_axes``  — rotary embedding with one position per axis.
+  * ``linear_attention`` — causal linear attention with a decay per head, by its
+    recurrence, and its gradients.
+  * ``cache_attention`` — attention of a few new tokens over a key/value cache.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against something other
 than itself (library special cases, closed forms, invariants, hand-derived
 worked examples under ``tests/golden/``). No function here is "parity
 unpinned".
 """
-from . import attention, attention_bwd, layouts, rope, schedule, sp_norm  # noqa: F401
+from . import (attention, attention_bwd, cache_attention, layouts, linear_attention, rope, rope_axes,  # noqa: F401
+               schedule, sp_norm)
