@@ -15,8 +15,9 @@
 // the even and the odd key tiles, each with its own maximum, sum and accumulator (joined
 // at the unit's end), so that one's softmax runs under the other's products.
 //
-// Cache rows past the last key are never read as values: their scores are set to -inf
-// and their rows of V are cleared in shared memory, so stale NaNs there do no harm.
+// Cache rows that no token sees, past the last key or a tree's padding, are never read as
+// values: their scores are set to -inf and their rows of V are cleared in shared memory, so
+// stale NaNs there do no harm.
 #include "cache_attn.h"
 
 #include <cmath>
@@ -189,6 +190,12 @@ __device__ __forceinline__ uint32_t keep_bits(uint64_t word, int lim) {
 __device__ __forceinline__ void mask_scores(uint32_t (&s)[32], uint32_t keep) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) s[j] = keep >> j & 1u ? s[j] : 0xff800000u;   // -inf
+}
+
+// OR over the lanes of a warp.
+__device__ __forceinline__ uint64_t any_lane(uint64_t x) {
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x));
+  return static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x >> 32))) << 32 | lo;
 }
 
 // Row r of the query tile: which token and query head, and where its results go.
@@ -380,6 +387,11 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
       if (p.own && cr.valid)
         word = p.tree == nullptr ? low_bits(cr.t + 1)
                                  : __ldg(p.tree + static_cast<int64_t>(sg.b) * p.T + cr.t) & low_bits(p.T);
+      uint64_t mine = low_bits(p.T);   // this lane's part of the drafted tokens that some token sees
+      if (p.own && p.tree != nullptr) {
+        const unsigned long long* words = p.tree + static_cast<int64_t>(sg.b) * p.T;
+        mine = (lane < p.T ? __ldg(words + lane) : 0) | (lane + 32 < p.T ? __ldg(words + lane + 32) : 0);
+      }
       // The accumulators and (max, sum) rows of the unit before have been read by both warpgroups.
       if (unit > 0 && !(ok = wait(sm.unit_done, unit - 1))) break;
       float m_run = -INFINITY, l_run = 0.f;
@@ -388,16 +400,21 @@ __global__ void __launch_bounds__(kCacheThreads, 1)
         ++s_cnt;
         tc_fence_after();
         const int k0 = (sg.t0 + i) * kTile;
-        if (keys - k0 < kTile) {
-          // The unit's last tile: clear the rows of V past its last key (its load is the
-          // last of the run), whatever the cache holds there.
-          const int idx = kv + 2 * sg.n - 1;
+        if (len - k0 < kTile) {
+          // A tile past the cached keys: clear the rows of V that no token sees, whatever the
+          // cache holds there. V of tile i is load 2 i + 2 of the piece, of its last tile the last.
+          const int idx = kv + min(2 * i + 2, 2 * sg.n - 1), end = min(keys - k0, kTile);
+          const uint64_t seen = any_lane(mine);
           if (!(ok = wait(sm.kv_full[idx % NS], idx / NS))) break;
           uint8_t* v = &sm.kv[idx % NS][0];
-          for (int e = row; e < (kTile - (keys - k0)) * 8 * C::kBlocks; e += 128) {
-            const int vec = e % (8 * C::kBlocks), r = keys - k0 + e / (8 * C::kBlocks);
+          auto clear = [&](int r, int vec) {
             *reinterpret_cast<uint4*>(v + (vec / 8) * kBlock + r * 128 + (vec % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          };
+          for (int e = row; e < (kTile - end) * 8 * C::kBlocks; e += 128)
+            clear(end + e / (8 * C::kBlocks), e % (8 * C::kBlocks));
+          if (p.own && (~seen & low_bits(p.T)))
+            for (int r = max(len - k0, 0) + row / (8 * C::kBlocks); r < end; r += 128 / (8 * C::kBlocks))
+              if (!(seen >> (k0 + r - len) & 1)) clear(r, row % (8 * C::kBlocks));
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         if (busy) {

@@ -463,9 +463,10 @@ CP_API int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* 
  * The state is held and summed in fp32; the decayed scores and the state that the
  * queries read are rounded to bf16 once, as tensor-core operands. Values must be
  * finite: within a chunk of 128 tokens a NaN or infinity also reaches the tokens before
- * it. One or two kernels; nothing is allocated; results do not depend on timing. Waits
- * that run out are reported by cp_attn_check. The plan's device must be current
- * (CP_ERR_INVALID_ARG).
+ * it. Outputs must not overlap inputs; calls that may overlap on the GPU need outputs and
+ * workspaces of their own. One or two kernels; nothing is allocated; results do not depend
+ * on timing. Waits that run out are reported by cp_attn_check. The plan's device must be
+ * current (CP_ERR_INVALID_ARG).
  */
 CP_API int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
                           const float* state_in, void* o, float* state_out, void* workspace, cp_stream_t stream);
@@ -495,7 +496,7 @@ CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
 /*
  * The recurrent form of the same operator: T <= 16 new tokens of each sequence (one
  * when decoding) on a state kept between calls, in fp32 throughout.
- *   q, k, v : bf16 [B][T][H][D], device;   o : bf16 [B][T][H][D], device (written)
+ *   q, k, v : bf16 [B][T][H][D], device;   o : the same (written; must not overlap them)
  *   state   : float32 [B][H][D][D], device, read and updated in place
  * D 64 or 128 (CP_ERR_UNSUPPORTED otherwise, and for T > 16); B = 0 or T = 0 does
  * nothing. Enqueued on `stream` of the current device.
@@ -511,7 +512,9 @@ CP_API int cp_linattn_step(int B, int T, int H, int D, const void* q, const void
  * b sees cache rows [0, lengths[b]) and row lengths[b] + u iff bit u of tree[b][t] is
  * set (set bit t for the token itself); query head h reads key/value head
  * h / (Hq / Hkv). Softmax, scale and lse as in cp_attn_fwd; a row that sees nothing gets
- * O = 0, lse = -inf. Cache rows from lengths[b] + T on may hold anything.
+ * O = 0, lse = -inf. Cache rows from lengths[b] + T on, and those of drafted tokens that no
+ * token of the sequence sees (a shorter tree padded to T with words of 0), may hold anything.
+ * The other rows must be finite: a NaN or infinity of V there reaches tokens that do not see it.
  *
  * A cache plan holds the sizes and a status word: B sequences (<= 1024), Hq query and
  * Hkv key/value heads (Hq a multiple, at most 128-fold), D 64 or 128, the cache's

@@ -147,6 +147,26 @@ def test_masked_rows_of_every_kind():
     assert_close(o[4:], lse[4:], ref, q[4:], k[4:, 130:132], v[4:, 130:132], [0], T)
 
 
+@pytest.mark.parametrize("T,used,n", [(20, 13, 100), (64, 3, 120), (64, 40, 128), (2, 0, 0), (64, 63, 200)])
+def test_padding_of_a_short_tree_may_hold_anything(T, used, n):
+    """Drafted tokens that no token sees: their words are 0 and their rows were never written,
+    in the tile that holds the last cached key and in the one after."""
+    B, Hq, Hkv, D, cap = 2, 4, 2, 128, 400
+    q, k, v, lens, words = case(B, T, Hq, Hkv, D, cap, (n, n + 5), seed=T + used)
+    for b, m in enumerate((n, n + 5)):
+        k[b, m + used:], v[b, m + used:], words[b, used:] = JUNK, JUNK, 0
+    hole = 1 if used > 2 else None                                  # a token that only itself would see
+    if hole is not None:
+        words &= ~(1 << hole)
+        k[0, n + hole], v[0, n + hole] = JUNK, JUNK
+    plan = cp.CachePlan(B, Hq, Hkv, D, cap, T)
+    o, lse = cp.cache_attn(plan, q.cuda(), k.cuda(), v.cuda(), lens.cuda(), words.cuda())
+    assert cp.cache_check(plan) == 0
+    clean = [torch.where(torch.isnan(x), torch.zeros_like(x), x) for x in (k, v)]
+    ref = CA.attend(q.double().numpy(), *(x.double().numpy() for x in clean), lens.tolist(), words_of(words))
+    assert_close(o, lse, ref, q, *clean, lens, T)
+
+
 def test_lengths_grow_on_the_device_in_a_graph():
     """Decoding as a captured step: the lengths are device memory, the replays follow them."""
     B, T, Hq, Hkv, D, cap = 2, 1, 8, 2, 64, 600
