@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     tmem_alloc(smem_addr(&sm.tmem_base), C::kTmemCols);
     tmem_relinquish();
   }
+  if (!OUT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the rows' launch may get ready
   if (warp == C::kTmaWarp && lane == 0) {
     prefetch_tensormap(&tm_a);
     prefetch_tensormap(&tm_b);
@@ -263,6 +264,8 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl ctl = wait_ctl(sm.wblk);
+  float* zt_smem = reinterpret_cast<float*>(&sm.tile[0][0]);   // D x D, rows D + 1 apart
+  static_assert(D * (D + 1) * 4 <= sizeof(sm.tile), "transposed state");
   const uint32_t tCw = tbase + kColCw, tS = tbase + kColS, tY = tbase + kColY;
   auto wait = [&](uint64_t& bar, int phase) { return all_ok(mbar_wait(smem_addr(&bar), phase & 1, ctl)); };
   auto tile_full = [&](int t) { return wait(sm.full[t % NT], t / NT); };
@@ -411,6 +414,8 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
           z[q] = w * __ldg(p.z0 + state0 + (p.z0_transposed ? row * D + col : col * D + row));
         }
       }
+      // Launched while the segments' states are still being computed.
+      if (p.nseg > 1) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int g = 0; g < seg; ++g) {
         const int end = walked_before(p, static_cast<int>(static_cast<int64_t>(g + 1) * p.nch / p.nseg));
         const float w = x == end ? 1.f : expf(static_cast<float>(ld * (x - end)));
@@ -527,6 +532,10 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < D / 8; ++q)
           dst[q * (2 * D)] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+        if (p.zseg_t != nullptr) {   // through the ring's memory, whose tiles have all been read
+#pragma unroll
+          for (int q = 0; q < D / 2; ++q) zt_smem[(col0 + q) * (D + 1) + row] = z[q];
+        }
       } else if (seg == p.nseg - 1 && p.z_out != nullptr) {
 #pragma unroll
         for (int q = 0; q < D / 2; ++q) p.z_out[state0 + static_cast<int64_t>(col0 + q) * D + row] = z[q];
@@ -672,6 +681,15 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, C::kTmemCols);
   }
+  if (!OUT && p.zseg_t != nullptr && warp < 8 && (warp & 3) * 32 < D) {
+    const int row = (warp & 3) * 32 + lane, grp = warp >> 2;
+    float4* dst = reinterpret_cast<float4*>(p.zseg_t + (static_cast<int64_t>(bh) * (p.nseg - 1) + seg) * (D * D)) +
+                  grp * D + row;
+    const float* src = zt_smem + row * (D + 1) + grp * (D / 2);
+#pragma unroll
+    for (int q = 0; q < D / 8; ++q)
+      dst[q * (2 * D)] = make_float4(src[4 * q], src[4 * q + 1], src[4 * q + 2], src[4 * q + 3]);
+  }
 }
 
 // ------------------------------------------------------------------ recurrent form
@@ -744,24 +762,37 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
 }
 
 template <int D, bool OUT, int TERMS>
-bool launch_lin(const LinLaunch& L, int segments, cudaStream_t stream) {
+bool launch_lin(const LinLaunch& L, int segments, bool early, cudaStream_t stream) {
   const size_t smem = sizeof(LinSmem<D, OUT, TERMS>) + 1024;
   auto kern = linattn_kernel<D, OUT, TERMS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return false;
-  kern<<<L.scans * L.scan[0].p.units * segments, LinCfg<D, OUT, TERMS>::kThreads, smem, stream>>>(L);
-  return cudaGetLastError() == cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L.scans * L.scan[0].p.units * segments);
+  cfg.blockDim = dim3(LinCfg<D, OUT, TERMS>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, L) == cudaSuccess;
 }
 
 // The launches of a forward or a backward: the segments' own states (all but the last),
-// then the rows.
+// then the rows. The backward's last scan takes its states from the one before, transposed.
 template <int D, int TERMS>
-bool launch_scans(const LinLaunch& L, cudaStream_t stream) {
-  const int nseg = L.scan[0].p.nseg;
-  if (nseg > 1 && !launch_lin<D, false, TERMS>(L, nseg - 1, stream)) return false;
-  return launch_lin<D, true, TERMS>(L, nseg, stream);
+bool launch_scans(LinLaunch& L, cudaStream_t stream) {
+  const int nseg = L.scan[0].p.nseg, scans = L.scans;
+  if (nseg > 1) {
+    L.scans = scans == 3 ? 2 : scans;
+    if (!launch_lin<D, false, TERMS>(L, nseg - 1, false, stream)) return false;
+    L.scans = scans;
+  }
+  return launch_lin<D, true, TERMS>(L, nseg, nseg > 1, stream);
 }
-bool launch_scans(const LinLaunch& L, int D, cudaStream_t stream) {
+bool launch_scans(LinLaunch& L, int D, cudaStream_t stream) {
   bool exact = false;   // a last state is asked for
   for (int i = 0; i < L.scans; ++i) exact = exact || L.scan[i].p.z_out != nullptr;
   if (D == 128) return exact ? launch_scans<128, 3>(L, stream) : launch_scans<128, 2>(L, stream);
@@ -794,14 +825,14 @@ LinView lin_view(const PlanView& v) {
 // launch 0.45. On 32 heads of 256 chunks (148 SMs) 4 segments take 362 us, 3 take 446, 9 take
 // 375, 2 take 652, and the model orders them so.
 constexpr int kMaxSegments = 64;
-int choose_segments(int64_t ctas, int nch, int sms) {
+int choose_segments(int64_t ctas, int64_t state_ctas, int nch, int sms) {
   int best = 1;
   double best_cost = 0;
   for (int s = 1; s <= nch && s <= kMaxSegments; ++s) {
     const double per = (nch + s - 1) / s;
     const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
     double cost = waves * (per + 2.5 + 0.35 * (s - 1));
-    if (s > 1) cost += static_cast<double>((ctas * (s - 1) + sms - 1) / sms) * (0.45 * per + 2.0);
+    if (s > 1) cost += static_cast<double>((state_ctas * (s - 1) + sms - 1) / sms) * (0.45 * per + 2.0);
     if (s == 1 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -814,10 +845,10 @@ size_t state_bytes(const PlanView& v, int nseg) {   // the segments' own states 
   return static_cast<size_t>(v.B) * v.H * (nseg - 1) * v.D * v.D * sizeof(float);
 }
 size_t fwd_workspace(const PlanView& v) {
-  return state_bytes(v, choose_segments(static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
+  return state_bytes(v, choose_segments(static_cast<int64_t>(v.B) * v.H, static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
 }
 size_t bwd_workspace(const PlanView& v) {
-  return 3 * state_bytes(v, choose_segments(3 * static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
+  return 3 * state_bytes(v, choose_segments(3 * static_cast<int64_t>(v.B) * v.H, 2 * static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
 }
 
 struct ScanCall {
@@ -858,6 +889,7 @@ bool make_scan(LinScan* L, const PlanView& v, const ScanCall& s, const float* lo
   p.z0 = s.z0;
   p.z_out = s.z_out;
   p.zseg = ws;
+  p.zseg_t = nullptr;
   p.y = static_cast<__nv_bfloat16*>(s.y);
   p.status = v.status;
   p.wait_limit_ns = kWaitLimitNs;
@@ -900,7 +932,7 @@ int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
   if (workspace == nullptr && fwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
-  const int nseg = choose_segments(static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
+  const int nseg = choose_segments(static_cast<int64_t>(pv.B) * pv.H, static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
   LinLaunch L;
   L.scans = 1;
   if (!make_scan(&L.scan[0], pv, {q, k, v, o, state_in, false, false, pv.scale, pv.scale, 1.f, state_out}, log_decay,
@@ -924,7 +956,7 @@ int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
   if (workspace == nullptr && bwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
-  const int nseg = choose_segments(3 * static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
+  const int nseg = choose_segments(3 * static_cast<int64_t>(pv.B) * pv.H, 2 * static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
   const size_t part = state_bytes(pv, nseg) / sizeof(float);
   const float sc = pv.scale;
   const ScanCall calls[3] = {{dout, v, k, dq, state_in, true, false, sc, sc, 1.f, nullptr},
@@ -936,6 +968,8 @@ int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void
     float* ws = part > 0 ? static_cast<float*>(workspace) + i * part : nullptr;
     if (!make_scan(&L.scan[i], pv, calls[i], log_decay, ws, nseg)) return CP_ERR_CUDA;
   }
+  // dk's state sums do_i q_i^T and dv's its transpose, in the same direction with the same weights.
+  if (part > 0) L.scan[1].p.zseg_t = L.scan[2].p.zseg;
   return launch_scans(L, pv.D, static_cast<cudaStream_t>(stream)) ? CP_OK : CP_ERR_CUDA;
 }
 

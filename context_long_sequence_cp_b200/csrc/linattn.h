@@ -24,6 +24,7 @@ struct LinParams {
   const float* z0;          // [B][H][D][D] or null
   float* z_out;             // [B][H][D][D] or null
   float* zseg;              // [units][nseg - 1][D][D]: each segment's own state
+  float* zseg_t;            // the same, transposed, for another scan (null: not wanted)
   __nv_bfloat16* y;
   int* status;
   uint64_t wait_limit_ns;
