@@ -15,6 +15,13 @@
 // the even and the odd key tiles, each with its own maximum, sum and accumulator (joined
 // at the unit's end), so that one's softmax runs under the other's products.
 //
+// Measured, 131040 cached keys, 8 key/value heads of 4 query heads, D = 128: 32 drafted
+// tokens 108 us, of them 97 in the first kernel (5.5 TB/s, 0.85 of the copy rate) and 9 in the
+// join, which can start only when the last CTA is done; one token 92 us. Sixteen sequences of
+// 0 to 8176 keys, 16 drafted tokens each: 66 us, 4.1 TB/s: about two units per CTA, whose start and end are not
+// hidden under another's products. P is kept to 2^-17 in two bf16 terms, so that a row of a
+// partial is as exact as its fp32 type says.
+//
 // Cache rows that no token sees, past the last key or a tree's padding, are never read as
 // values: their scores are set to -inf and their rows of V are cleared in shared memory, so
 // stale NaNs there do no harm.

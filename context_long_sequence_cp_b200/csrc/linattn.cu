@@ -21,8 +21,19 @@
 //
 // A CTA walks a run of chunks ("segment") of one (batch, head); Z stays in the registers
 // of eight warps in fp32. Sequences with few (batch, head) are cut into segments: a first
-// launch (OUT = false) computes each segment's own state, and the second joins those
-// before it at its start.
+// launch (OUT = false) computes each segment's own state, and the second, launched early,
+// joins those before it at its start.
+//
+// Bound. The forward cannot do without 8 bytes per element (164 us for 32768 tokens, 32 heads,
+// D = 128, at the card's copy rate); the two launches read B and C twice. Measured there:
+// 320 us, 75 of them for the segments' states, and 363 (125 and 237) where a last state is
+// asked for; with loads that all hit L2 302, so HBM is not what bounds it. A chunk takes
+// ~5600 cycles of an SM, the tensor core ~2400 of them: the chain of the state's warps
+// (weight C, the product, add, publish Z) and that of the score warps (scores, P, the
+// product, output) meet once per chunk, and each is about that long. Not kept, measured:
+// eight score warps (333 us: 96 registers a thread spill), output staged over A for a ring of
+// six tiles (323), Z published after the next weighting (321), loads of TMEM a block ahead
+// (319), parts of a segment's state on CTAs of their own (322).
 //
 // Precision. Where the last state is asked for, the state is exact to fp32: the weighted
 // rows of C are split into three bf16 terms (8 + 8 + 8 bits of the fp32 product) multiplied
