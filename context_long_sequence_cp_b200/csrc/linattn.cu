@@ -47,7 +47,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <cstring>
+#include <initializer_list>
 
 #include "cp_attn.h"
 #include "linattn.h"
@@ -918,6 +918,14 @@ bool make_scan(LinScan* L, const PlanView& v, const ScanCall& s, const float* lo
   return true;
 }
 
+// One of the outputs is one of the inputs: other CTAs would read rows already written.
+bool aliased(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o != nullptr && o == i) return true;
+  return false;
+}
+
 // Arguments common to the forward and the backward.
 int check_plan(cp_attn_plan_t plan, PlanView* v) {
   const int rc = plan_view(plan, v);
@@ -954,6 +962,7 @@ int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
   if (workspace == nullptr && fwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
+  if (aliased({o, state_out}, {q, k, v, log_decay, state_in})) return CP_ERR_INVALID_ARG;
   const int nseg = choose_segments(static_cast<int64_t>(pv.B) * pv.H, static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
   LinLaunch L;
   L.scans = 1;
@@ -978,6 +987,7 @@ int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
   if (workspace == nullptr && bwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
+  if (aliased({dq, dk, dv, dstate_in}, {q, k, v, log_decay, dout, state_in, dstate_out})) return CP_ERR_INVALID_ARG;
   const int nseg = choose_segments(3 * static_cast<int64_t>(pv.B) * pv.H, 2 * static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
   const size_t part = state_bytes(pv, nseg) / sizeof(float);
   const float sc = pv.scale;
@@ -1011,6 +1021,7 @@ int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, co
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return CP_ERR_CUDA;
+  if (aliased({o}, {q, k, v})) return CP_ERR_INVALID_ARG;
   LinStepParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);

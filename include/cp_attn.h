@@ -463,10 +463,11 @@ CP_API int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* 
  * The state is held and summed in fp32; the decayed scores and the state that the
  * queries read are rounded to bf16 once, as tensor-core operands. Values must be
  * finite: within a chunk of 128 tokens a NaN or infinity also reaches the tokens before
- * it. Outputs must not overlap inputs; calls that may overlap on the GPU need outputs and
- * workspaces of their own. One or two kernels; nothing is allocated; results do not depend
- * on timing. Waits that run out are reported by cp_attn_check. The plan's device must be
- * current (CP_ERR_INVALID_ARG).
+ * it. Outputs must not overlap inputs (the same pointer as both: CP_ERR_INVALID_ARG);
+ * calls that may overlap on the GPU need outputs and workspaces of their own. One or
+ * two kernels; nothing is allocated; results do not depend on timing. Waits that run
+ * out are reported by cp_attn_check. The plan's device must be current
+ * (CP_ERR_INVALID_ARG).
  */
 CP_API int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
                           const float* state_in, void* o, float* state_out, void* workspace, cp_stream_t stream);

@@ -280,3 +280,53 @@ def test_refusals_with_a_device():
         cp.linattn_fwd(plan, q.transpose(2, 3), q, q, ld)
     with pytest.raises(cp.CpAttnError):
         cp.linattn_step(*([torch.zeros(1, 17, 2, 64, dtype=torch.bfloat16, device="cuda")] * 3), ld, st)
+
+
+def test_outputs_over_inputs_are_refused():
+    """Other CTAs read the rows and states that an output in place would overwrite."""
+    plan = cp.Plan(1, 2, 300, 64, 1, True, "contiguous")
+    q, k, v, do = (torch.zeros(1, 1, 300, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    ld, st = torch.zeros(2, device="cuda"), torch.zeros(1, 2, 64, 64, device="cuda")
+    for x in (q, k, v):
+        with pytest.raises(cp.CpAttnError):
+            cp.linattn_fwd(plan, q, k, v, ld, o=x)
+    new = [torch.empty_like(q) for _ in range(3)]
+    ptr = lambda t: None if t is None else t.data_ptr()
+    ws = torch.empty(plan.linattn_workspace_bytes() + 16, dtype=torch.uint8, device="cuda")
+    for grads, dsi in ((new, st), ([do] + new[1:], None), ([new[0], q, new[2]], None), (new[:2] + [k], None)):
+        assert cp.lib().cp_linattn_bwd(plan.handle, ptr(q), ptr(k), ptr(v), ptr(ld), ptr(do), ptr(st), None,
+                                       *(ptr(g) for g in grads), ptr(dsi), ptr(ws), None) == -1
+    a = [torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    for x in a:
+        with pytest.raises(cp.CpAttnError):
+            cp.linattn_step(*a, ld, st, o=x)
+
+
+def test_a_long_sequence_of_one_head_and_its_gradients():
+    """Many segments, whose states dv's scan takes from dk's; and the state chained by hand."""
+    B, H, S, D = 1, 1, 6200, 128
+    q, k, v, do, s0, ds = inputs(B, S, H, D, seed=5)
+    ld = torch.tensor([-0.002])
+    plan = cp.Plan(B, H, S, D, 1, True, "contiguous")
+    assert plan.linattn_workspace_bytes() > 0
+    lay = lambda t: G.to_layout(t, 1, "contiguous").cuda()
+    dev = [lay(t) for t in (q, k, v, do)]
+    dq, dk, dv, dsi = cp.linattn_bwd(plan, *dev[:3], ld.cuda(), dev[3], state_in=s0.cuda(), dstate_out=ds.cuda(),
+                                     want_dstate=True)
+    assert cp.check(plan) == 0
+    scale = 1 / D ** 0.5
+    w = torch.exp(ld.double()[0] * (torch.arange(S, dtype=torch.float64)[:, None] - torch.arange(S, dtype=torch.float64)))
+    m = torch.tril(w) * scale
+    Q, K, V, DO = (t[0, :, 0].double() for t in (q, k, v, do))
+    G1, S0 = ds[0, 0].double(), s0[0, 0].double()
+    up = torch.exp(ld.double()[0] * (torch.arange(S, dtype=torch.float64) + 1))[:, None]
+    down = torch.exp(ld.double()[0] * (S - 1 - torch.arange(S, dtype=torch.float64)))[:, None]
+    a, b = (DO @ V.T) * m, (Q @ K.T) * m
+    refs = (a @ K + scale * up * (DO @ S0.T), a.T @ Q + down * (V @ G1.T), b.T @ DO + down * (K @ G1),
+            scale * (up * Q).T @ DO + torch.exp(ld.double()[0] * S) * G1)
+    mags = (a.abs() @ K.abs() + scale * up * (DO.abs() @ S0.abs().T), a.abs().T @ Q.abs() + down * (V.abs() @ G1.abs().T),
+            b.abs().T @ DO.abs() + down * (K.abs() @ G1.abs()),
+            scale * (up * Q).abs().T @ DO.abs() + torch.exp(ld.double()[0] * S) * G1.abs())
+    for got, ref, mag, name in zip((dq, dk, dv), refs, mags, ("dq", "dk", "dv")):
+        assert_rows(G.from_layout(got.cpu(), 1, "contiguous")[0, :, 0], ref.numpy(), mag.numpy(), name)
+    assert_state(dsi[0, 0], refs[3].numpy(), mags[3].numpy(), S, "dstate_in")
