@@ -844,8 +844,9 @@ LinView lin_view(const PlanView& v) {
 // Segments a sequence is cut into, for `ctas` scans x (batch, head) of nch chunks. Modelled
 // time in chunks of the output launch (3.1 us each): a wave costs its chunks, about 2.5 more
 // to fill and drain, and 0.35 for each earlier segment's state to join; a chunk of the state
-// launch 0.45. On 32 heads of 256 chunks (148 SMs) 4 segments take 362 us, 3 take 446, 9 take
-// 375, 2 take 652, and the model orders them so.
+// launch 0.45. Measured on 148 SMs, us, the model's choice first: 32 heads of 256 chunks 4
+// segments 312, 3 394, 5 418, 9 322, 1 763; the backward of 4 heads of 256 chunks 12 133, 9 158,
+// 16 183, 1 767; 8 heads of 64 chunks 12 52.5, 16 50.8, 8 55.5, 1 202.
 constexpr int kMaxSegments = 64;
 int choose_segments(int64_t ctas, int64_t state_ctas, int nch, int sms) {
   int best = 1;

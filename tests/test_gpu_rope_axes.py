@@ -107,3 +107,11 @@ def test_given_output_other_stream_and_graph():
     pos.add_(3)
     graph.replay()
     assert torch.equal(out, cp.rope_axes(plan, y, pos, [16, 16]))
+
+
+def test_in_place_is_refused():
+    plan = cp.Plan(1, 2, 64, 64, 1, True, "contiguous")
+    x = torch.zeros(1, 64, 2, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(1, 1, 64, dtype=torch.int32, device="cuda")
+    with pytest.raises(cp.CpAttnError):
+        cp.rope_axes(plan, x, pos, [32], out=x.view(1, 1, 64, 2, 64))
