@@ -7,7 +7,6 @@ raises when the library is missing, and every call raises on a non-zero status.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -119,11 +118,6 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _device(index):
-    """Context with that device current (nothing without one)."""
-    return contextlib.nullcontext() if index is None else torch.cuda.device(index)
-
-
 class Plan:
     """A context-parallel attention plan (wraps ``cp_attn_plan``)."""
 
@@ -132,7 +126,6 @@ class Plan:
         self.B, self.H, self.S, self.D, self.N = B, H, S, D, N
         self.causal, self.layout = bool(causal), layout
         self.scale = softmax_scale if softmax_scale > 0 else 1.0 / math.sqrt(D)
-        self.device = torch.cuda.current_device() if torch.cuda.is_available() else None
         self._linattn_ws = None
         h = ctypes.c_void_p()
         _check("cp_attn_plan", lib().cp_attn_plan(ctypes.byref(h), B, H, S, D, N, int(bool(causal)),
@@ -213,8 +206,7 @@ class Plan:
 
     def linattn_workspace_bytes(self) -> int:
         if self._linattn_ws is None:
-            with _device(self.device):
-                self._linattn_ws = int(lib().cp_linattn_workspace_bytes(self._h))
+            self._linattn_ws = int(lib().cp_linattn_workspace_bytes(self._h))
         return self._linattn_ws
 
     def workspace_bytes(self, with_partials: bool = False) -> int:

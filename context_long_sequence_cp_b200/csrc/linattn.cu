@@ -927,13 +927,16 @@ bool aliased(std::initializer_list<const void*> outs, std::initializer_list<cons
   return false;
 }
 
-// Arguments common to the forward and the backward.
+bool supported(const PlanView& v) {
+  if (v.layout == CP_LAYOUT_ULYSSES || !v.causal) return false;
+  // one CTA per scan, (batch, head) and segment, indexed in int32
+  return static_cast<int64_t>(v.B) * v.H <= (int64_t(1) << 29) / kMaxSegments;
+}
+
+// The plan of a forward or a backward.
 int check_plan(cp_attn_plan_t plan, PlanView* v) {
   const int rc = plan_view(plan, v);
-  if (v->layout == CP_LAYOUT_ULYSSES || !v->causal) return CP_ERR_UNSUPPORTED;
-  // one CTA per scan, (batch, head) and segment, indexed in int32
-  if (static_cast<int64_t>(v->B) * v->H > (int64_t(1) << 29) / kMaxSegments) return CP_ERR_UNSUPPORTED;
-  return rc;
+  return supported(*v) ? rc : CP_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -945,8 +948,10 @@ using namespace cpattn;
 extern "C" {
 
 size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan) {
+  if (plan == nullptr) return 0;
   PlanView v;
-  if (plan == nullptr || check_plan(plan, &v) != CP_OK) return 0;
+  plan_view(plan, &v);   // the sizes, whichever device is current
+  if (!supported(v)) return 0;
   const size_t f = fwd_workspace(v), b = bwd_workspace(v);
   return f > b ? f : b;
 }

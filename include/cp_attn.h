@@ -491,7 +491,8 @@ CP_API int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, con
                           void* dv, float* dstate_in, void* workspace, cp_stream_t stream);
 
 /* Workspace bytes of cp_linattn_fwd and cp_linattn_bwd on this plan (0 where none is
- * needed, and for a plan they do not support). */
+ * needed, and for a plan they do not support). They depend on the plan alone, not on the
+ * device that is current. */
 CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
 
 /*

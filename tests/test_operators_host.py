@@ -169,3 +169,15 @@ def test_python_refuses_what_does_not_fit():
         cp.cache_attn(c, bf(1, 3, 4, 64), kv, kv, n)
     with pytest.raises(ValueError, match="CUDA"):
         cp.linattn_step(bf(1, 1, 2, 64), bf(1, 1, 2, 64), bf(1, 1, 2, 64), ld, st)
+
+
+def test_linattn_workspace_depends_on_the_plan_alone():
+    """Sized with any device current, or none: a caller that lays out its buffers first gets the
+    bytes that the call will use. 8 heads of 64 chunks: 16 segments forward, 15 of whose states
+    are kept (the backward: 6, three scans of 5)."""
+    plan = cp.Plan(1, 8, 64 * 128, 64, 1, True, "contiguous")
+    sms = 148 if not torch.cuda.is_available() else torch.cuda.get_device_properties(0).multi_processor_count
+    n = int(cp.lib().cp_linattn_workspace_bytes(plan.handle))
+    assert n > 0 and n % (8 * 64 * 64 * 4) == 0
+    assert sms != 148 or n == 15 * 8 * 64 * 64 * 4
+    assert plan.linattn_workspace_bytes() == n
