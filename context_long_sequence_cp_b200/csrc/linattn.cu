@@ -737,8 +737,11 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
     sqk[t][d] = make_float2(__bfloat162float(p.q[at]) * p.scale, __bfloat162float(p.k[at]));
     if (d < CW) sv[t][d] = __bfloat162float(p.v[at + sl * CW]);
   }
-  const float dec = expf(__ldg(p.log_decay + h));
-  const uint64_t dec2 = f2_pack(dec, dec);
+  // d as an fp32 pair, as in the chunked form: one fp32 number is off by up to 2^-25 of it, the same
+  // way at every call, and a state kept over thousands of tokens would show that.
+  const double d = decay_pow(static_cast<double>(__ldg(p.log_decay + h)), 1);
+  const float hi = static_cast<float>(d), lo = static_cast<float>(d - static_cast<double>(hi));
+  const uint64_t hi2 = f2_pack(hi, hi), lo2 = f2_pack(lo, lo);
   __syncthreads();
   for (int t0 = 0; t0 < p.T; t0 += kGroup) {
     const int t1 = min(t0 + kGroup, p.T);
@@ -750,8 +753,9 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
       for (int r = 0; r < RPT; ++r) {
         const float2 qk = sqk[t][rg + r * RG];
         const uint64_t qq = f2_pack(qk.x, qk.x), kk = f2_pack(qk.y, qk.y);
-        const uint64_t s0 = f2_fma(f2_pack(s[r].x, s[r].y), dec2, f2_mul(kk, v0));
-        const uint64_t s1 = f2_fma(f2_pack(s[r].z, s[r].w), dec2, f2_mul(kk, v1));
+        const uint64_t z0 = f2_pack(s[r].x, s[r].y), z1 = f2_pack(s[r].z, s[r].w);
+        const uint64_t s0 = f2_fma(z0, hi2, f2_fma(z0, lo2, f2_mul(kk, v0)));
+        const uint64_t s1 = f2_fma(z1, hi2, f2_fma(z1, lo2, f2_mul(kk, v1)));
         o0 = f2_fma(qq, s0, o0);
         o1 = f2_fma(qq, s1, o1);
         f2_unpack(s0, s[r].x, s[r].y);
@@ -1041,8 +1045,8 @@ int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, co
   const int64_t heads = static_cast<int64_t>(B) * H;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // A whole head per CTA where there is one for each SM; else 32 columns each, for more CTAs.
-  // Measured whole and cut on 148 SMs, D = 128: 32 heads 3.2 and 2.4 us (16 tokens: 8.7 and 6.3),
-  // 148 heads 3.7 and 3.9 (9.2 and 11.6), 2048 heads 43.3 and 45.0 (97 and 129).
+  // Measured whole and cut on 148 SMs, D = 128: 32 heads 3.4 and 2.3 us (16 tokens: 10.2 and 6.6),
+  // 148 heads 3.7 and 3.5 (10.6 and 12.9), 2048 heads 43.4 and 41.5 (114 and 147).
   const bool wide = heads >= sms;
   const int grid = static_cast<int>(heads * (wide ? 1 : D / 32));
   if (D == 128) {

@@ -497,7 +497,9 @@ CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
 
 /*
  * The recurrent form of the same operator: T <= 16 new tokens of each sequence (one
- * when decoding) on a state kept between calls, in fp32 throughout.
+ * when decoding) on a state kept between calls, in fp32 throughout. The decay itself is
+ * exact to 2^-48; each token rounds the state to fp32 once, so what a decay nearer to 1
+ * than 2^-25 (log_decay above -3e-8) takes off may be rounded away.
  *   q, k, v : bf16 [B][T][H][D], device;   o : the same (written; must not overlap them)
  *   state   : float32 [B][H][D][D], device, read and updated in place
  * D 64 or 128 (CP_ERR_UNSUPPORTED otherwise, and for T > 16); B = 0 or T = 0 does

@@ -330,3 +330,34 @@ def test_a_long_sequence_of_one_head_and_its_gradients():
     for got, ref, mag, name in zip((dq, dk, dv), refs, mags, ("dq", "dk", "dv")):
         assert_rows(G.from_layout(got.cpu(), 1, "contiguous")[0, :, 0], ref.numpy(), mag.numpy(), name)
     assert_state(dsi[0, 0], refs[3].numpy(), mags[3].numpy(), S, "dstate_in")
+
+
+def test_step_keeps_slow_decays_over_thousands_of_tokens():
+    """A state kept over 4096 tokens. A token's update is d S + k v^T rounded to fp32: with d as a
+    pair of fp32 numbers (2^-48 of d) the inner sum k v^T + lo S is rounded once, by at most 2^-24
+    of its value (k v^T itself is exact), and the outer one once, by at most half a step of the
+    new state. Later decays do not enlarge these. They need not be of either sign by chance: where
+    the state and the row lie on one grid, what d takes off a token may be rounded away each time
+    (all of it, for d nearer to 1 than half a step), so they are added as they are, in the 2-norm:
+        |error| <= sum_t (|half steps of S_t| + 2^-24 (|k_t v_t^T| + 2^-24 |S_t|)),
+    with 1% for entries whose computed value lies across a power of two. A decay kept as one fp32
+    exponential is off by up to 2^-23 of d, twice a half step, and exceeds this sum."""
+    S, H, D = 4096, 4, 64
+    q, k, v, _, s0, _ = (t.cuda() for t in inputs(1, S, H, D, seed=12))
+    ld = torch.tensor([-1e-6, -2e-8, -1e-4, 0.0], device="cuda")
+    one, many = s0.clone(), s0.clone()
+    for t in range(S):
+        cp.linattn_step(*(x[:, t:t + 1] for x in (q, k, v)), ld, one)
+    for t in range(0, S, 16):
+        cp.linattn_step(*(x[:, t:t + 16] for x in (q, k, v)), ld, many)
+    assert torch.equal(one, many)
+    ref, d = s0.double(), torch.exp(ld.double())[None, :, None, None]
+    norm = lambda x: x.square().sum((0, 2, 3)).sqrt()
+    bound = torch.zeros(H, dtype=torch.float64, device="cuda")
+    for t in range(S):
+        new = k[:, t].double()[..., :, None] * v[:, t].double()[..., None, :]
+        ref = d * ref + new
+        half_step = torch.exp2(torch.floor(torch.log2(ref.abs().clamp(min=2.0 ** -126))) - 24)
+        bound += 1.01 * norm(half_step) + 2.0 ** -24 * (norm(new) + 2.0 ** -24 * norm(ref))
+    err = norm(one.double() - ref)
+    assert torch.all(err <= bound), (err / bound).tolist()
