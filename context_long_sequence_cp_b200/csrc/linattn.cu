@@ -46,6 +46,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 #include <initializer_list>
 
@@ -710,16 +711,23 @@ __global__ void __launch_bounds__(LinCfg<D, OUT, TERMS>::kThreads, 1)
 // rows rg, rg + RG, ... of four columns in registers; each token's output is summed
 // over a warp's row groups by shuffles and over the warps through shared memory,
 // four tokens at a time.
+constexpr int kStepGroup = 4;   // tokens whose sums are joined at a time
+template <int D, int CW>
+struct alignas(16) StepSmem {
+  float2 qk[kLinStepMaxT][D];
+  float v[kLinStepMaxT][CW];       // v and red are also read and written as float4
+  float red[kStepGroup][8][CW];
+};
+
 template <int D, int CW>
 __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p) {
   constexpr int CG = CW / 4;        // column groups of 4
   constexpr int RG = 256 / CG;      // row groups
   constexpr int RPT = D / RG;       // rows per thread
   static_assert(RPT >= 1 && CG <= 32, "tile");
-  constexpr int kGroup = 4;         // tokens whose sums are joined at a time
-  __shared__ float2 sqk[kLinStepMaxT][D];
-  __shared__ float sv[kLinStepMaxT][CW];
-  __shared__ float red[kGroup][8][CW];
+  using Smem = StepSmem<D, CW>;
+  static_assert(offsetof(Smem, v) % 16 == 0 && offsetof(Smem, red) % 16 == 0 && CW % 4 == 0, "float4 accesses");
+  __shared__ Smem sm;
   constexpr int kSl = D / CW;
   const int sl = static_cast<int>(blockIdx.x) % kSl;
   const int64_t bh = blockIdx.x / kSl;
@@ -734,8 +742,8 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
   for (int i = threadIdx.x; i < p.T * D; i += 256) {
     const int t = i / D, d = i % D;
     const int64_t at = ((b * p.T + t) * p.H + h) * D + d;
-    sqk[t][d] = make_float2(__bfloat162float(p.q[at]) * p.scale, __bfloat162float(p.k[at]));
-    if (d < CW) sv[t][d] = __bfloat162float(p.v[at + sl * CW]);
+    sm.qk[t][d] = make_float2(__bfloat162float(p.q[at]) * p.scale, __bfloat162float(p.k[at]));
+    if (d < CW) sm.v[t][d] = __bfloat162float(p.v[at + sl * CW]);
   }
   // d as an fp32 pair, as in the chunked form: one fp32 number is off by up to 2^-25 of it, the same
   // way at every call, and a state kept over thousands of tokens would show that.
@@ -743,15 +751,15 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
   const float hi = static_cast<float>(d), lo = static_cast<float>(d - static_cast<double>(hi));
   const uint64_t hi2 = f2_pack(hi, hi), lo2 = f2_pack(lo, lo);
   __syncthreads();
-  for (int t0 = 0; t0 < p.T; t0 += kGroup) {
-    const int t1 = min(t0 + kGroup, p.T);
+  for (int t0 = 0; t0 < p.T; t0 += kStepGroup) {
+    const int t1 = min(t0 + kStepGroup, p.T);
     for (int t = t0; t < t1; ++t) {
-      const float4 v = *reinterpret_cast<const float4*>(&sv[t][cg * 4]);
+      const float4 v = *reinterpret_cast<const float4*>(&sm.v[t][cg * 4]);
       const uint64_t v0 = f2_pack(v.x, v.y), v1 = f2_pack(v.z, v.w);
       uint64_t o0 = f2_pack(0.f, 0.f), o1 = o0;
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        const float2 qk = sqk[t][rg + r * RG];
+        const float2 qk = sm.qk[t][rg + r * RG];
         const uint64_t qq = f2_pack(qk.x, qk.x), kk = f2_pack(qk.y, qk.y);
         const uint64_t z0 = f2_pack(s[r].x, s[r].y), z1 = f2_pack(s[r].z, s[r].w);
         const uint64_t s0 = f2_fma(z0, hi2, f2_fma(z0, lo2, f2_mul(kk, v0)));
@@ -771,14 +779,14 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
         o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
         o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
       }
-      if (lane < CG) *reinterpret_cast<float4*>(&red[t - t0][warp][lane * 4]) = o;
+      if (lane < CG) *reinterpret_cast<float4*>(&sm.red[t - t0][warp][lane * 4]) = o;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < (t1 - t0) * CW; i += 256) {
       const int t = t0 + i / CW, c = i % CW;
       float y = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) y += red[t - t0][w][c];
+      for (int w = 0; w < 8; ++w) y += sm.red[t - t0][w][c];
       p.o[((b * p.T + t) * p.H + h) * D + sl * CW + c] = __float2bfloat16_rn(y);
     }
     if (t1 < p.T) __syncthreads();   // the sums have been read before the next group's are written
