@@ -442,6 +442,8 @@ def _enqueue(device, stream, body):
             return body(torch._C._cuda_getCurrentRawStream(device.index))
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         return body(stream.cuda_stream)
 

@@ -181,3 +181,12 @@ def test_linattn_workspace_depends_on_the_plan_alone():
     assert n > 0 and n % (8 * 64 * 64 * 4) == 0
     assert sms != 148 or n == 15 * 8 * 64 * 64 * 4
     assert plan.linattn_workspace_bytes() == n
+
+
+def test_python_refuses_a_stream_of_another_device():
+    """Entering such a stream would make its device current, and the kernel would run there on the
+    tensors' addresses."""
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream"):
+        cp._enqueue(torch.device("cuda", 0), Stream(), lambda s: pytest.fail("launched"))
