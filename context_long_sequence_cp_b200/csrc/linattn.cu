@@ -48,7 +48,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <initializer_list>
 
 #include "cp_attn.h"
 #include "linattn.h"
@@ -876,14 +875,17 @@ int choose_segments(int64_t ctas, int64_t state_ctas, int nch, int sms) {
   return best;
 }
 
+size_t tensor_bytes(const PlanView& v) { return sizeof(__nv_bfloat16) * v.B * v.S * v.H * v.D; }
 size_t state_bytes(const PlanView& v, int nseg) {   // the segments' own states of one scan
   return static_cast<size_t>(v.B) * v.H * (nseg - 1) * v.D * v.D * sizeof(float);
 }
-size_t fwd_workspace(const PlanView& v) {
-  return state_bytes(v, choose_segments(static_cast<int64_t>(v.B) * v.H, static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
+int fwd_segments(const PlanView& v) {
+  const int64_t units = static_cast<int64_t>(v.B) * v.H;
+  return choose_segments(units, units, lin_view(v).nch, v.sms);
 }
-size_t bwd_workspace(const PlanView& v) {
-  return 3 * state_bytes(v, choose_segments(3 * static_cast<int64_t>(v.B) * v.H, 2 * static_cast<int64_t>(v.B) * v.H, lin_view(v).nch, v.sms));
+int bwd_segments(const PlanView& v) {
+  const int64_t units = static_cast<int64_t>(v.B) * v.H;
+  return choose_segments(3 * units, 2 * units, lin_view(v).nch, v.sms);
 }
 
 struct ScanCall {
@@ -931,14 +933,6 @@ bool make_scan(LinScan* L, const PlanView& v, const ScanCall& s, const float* lo
   return true;
 }
 
-// One of the outputs is one of the inputs: other CTAs would read rows already written.
-bool aliased(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
-  for (const void* o : outs)
-    for (const void* i : ins)
-      if (o != nullptr && o == i) return true;
-  return false;
-}
-
 bool supported(const PlanView& v) {
   if (v.layout == CP_LAYOUT_ULYSSES || !v.causal) return false;
   // one CTA per scan, (batch, head) and segment, indexed in int32
@@ -964,7 +958,7 @@ size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan) {
   PlanView v;
   plan_view(plan, &v);   // the sizes, whichever device is current
   if (!supported(v)) return 0;
-  const size_t f = fwd_workspace(v), b = bwd_workspace(v);
+  const size_t f = state_bytes(v, fwd_segments(v)), b = 3 * state_bytes(v, bwd_segments(v));
   return f > b ? f : b;
 }
 
@@ -979,9 +973,14 @@ int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   PlanView pv;
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
-  if (workspace == nullptr && fwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
-  if (aliased({o, state_out}, {q, k, v, log_decay, state_in})) return CP_ERR_INVALID_ARG;
-  const int nseg = choose_segments(static_cast<int64_t>(pv.B) * pv.H, static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
+  const int nseg = fwd_segments(pv);
+  const size_t ws_bytes = state_bytes(pv, nseg);
+  if (workspace == nullptr && ws_bytes > 0) return CP_ERR_WORKSPACE;
+  // Other CTAs would read rows already written, or write the same ones.
+  const size_t t = tensor_bytes(pv), z = state_bytes(pv, 2), ld = pv.H * sizeof(float);
+  if (overlaps({{o, t}, {state_out, z}, {workspace, ws_bytes}},
+               {{q, t}, {k, t}, {v, t}, {log_decay, ld}, {state_in, z}}))
+    return CP_ERR_INVALID_ARG;
   LinLaunch L;
   L.scans = 1;
   if (!make_scan(&L.scan[0], pv, {q, k, v, o, state_in, false, false, pv.scale, pv.scale, 1.f, state_out}, log_decay,
@@ -1004,10 +1003,13 @@ int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void
   PlanView pv;
   int rc = check_plan(plan, &pv);
   if (rc != CP_OK) return rc;
-  if (workspace == nullptr && bwd_workspace(pv) > 0) return CP_ERR_WORKSPACE;
-  if (aliased({dq, dk, dv, dstate_in}, {q, k, v, log_decay, dout, state_in, dstate_out})) return CP_ERR_INVALID_ARG;
-  const int nseg = choose_segments(3 * static_cast<int64_t>(pv.B) * pv.H, 2 * static_cast<int64_t>(pv.B) * pv.H, lin_view(pv).nch, pv.sms);
-  const size_t part = state_bytes(pv, nseg) / sizeof(float);
+  const int nseg = bwd_segments(pv);
+  const size_t part_bytes = state_bytes(pv, nseg), part = part_bytes / sizeof(float);
+  if (workspace == nullptr && part > 0) return CP_ERR_WORKSPACE;
+  const size_t t = tensor_bytes(pv), z = state_bytes(pv, 2), ld = pv.H * sizeof(float);
+  if (overlaps({{dq, t}, {dk, t}, {dv, t}, {dstate_in, z}, {workspace, 3 * part_bytes}},
+               {{q, t}, {k, t}, {v, t}, {log_decay, ld}, {dout, t}, {state_in, z}, {dstate_out, z}}))
+    return CP_ERR_INVALID_ARG;
   const float sc = pv.scale;
   const ScanCall calls[3] = {{dout, v, k, dq, state_in, true, false, sc, sc, 1.f, nullptr},
                              {v, dout, q, dk, dstate_out, true, true, sc, 1.f, sc, nullptr},
@@ -1039,7 +1041,9 @@ int cp_linattn_step(int B, int T, int H, int D, const void* q, const void* k, co
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return CP_ERR_CUDA;
-  if (aliased({o}, {q, k, v})) return CP_ERR_INVALID_ARG;
+  const size_t t = sizeof(__nv_bfloat16) * B * T * H * D;
+  if (overlaps({{o, t}, {state, sizeof(float) * B * H * D * D}}, {{q, t}, {k, t}, {v, t}, {log_decay, H * sizeof(float)}}))
+    return CP_ERR_INVALID_ARG;
   LinStepParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);

@@ -458,12 +458,12 @@ CP_API int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* 
  *               state before token 0, device; NULL for zero
  *   o         : bf16, q's layout, device (written)
  *   state_out : float32 [B][H][D][D], the state after the last token, device (written);
- *               may be NULL; must not overlap state_in
+ *               may be NULL
  *   workspace : device, cp_linattn_workspace_bytes(plan) bytes (NULL if 0)
  * The state is held and summed in fp32; the decayed scores and the state that the
  * queries read are rounded to bf16 once, as tensor-core operands. Values must be
  * finite: within a chunk of 128 tokens a NaN or infinity also reaches the tokens before
- * it. Outputs must not overlap inputs (the same pointer as both: CP_ERR_INVALID_ARG);
+ * it. Outputs and the workspace must not overlap inputs nor one another (CP_ERR_INVALID_ARG);
  * calls that may overlap on the GPU need outputs and workspaces of their own. One or
  * two kernels; nothing is allocated; results do not depend on timing. Waits that run
  * out are reported by cp_attn_check. The plan's device must be current
@@ -482,9 +482,9 @@ CP_API int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, con
  *   state_in   : the forward's, or NULL
  *   dstate_out : float32 [B][H][D][D], the gradient of state_out, or NULL for zero
  *   dq, dk, dv : bf16, q's layout, device (written)
- *   dstate_in  : float32 [B][H][D][D], device (written); may be NULL; must not overlap
- *                dstate_out
+ *   dstate_in  : float32 [B][H][D][D], device (written); may be NULL
  *   workspace  : device, cp_linattn_workspace_bytes(plan) bytes (NULL if 0)
+ * Overlaps are refused as there.
  */
 CP_API int cp_linattn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
                           const void* dout, const float* state_in, const float* dstate_out, void* dq, void* dk,
@@ -500,8 +500,9 @@ CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
  * when decoding) on a state kept between calls, in fp32 throughout. The decay itself is
  * exact to 2^-48; each token rounds the state to fp32 once, so what a decay nearer to 1
  * than 2^-25 (log_decay above -3e-8) takes off may be rounded away.
- *   q, k, v : bf16 [B][T][H][D], device;   o : the same (written; must not overlap them)
+ *   q, k, v : bf16 [B][T][H][D], device;   o : the same (written)
  *   state   : float32 [B][H][D][D], device, read and updated in place
+ * o and state must not overlap the inputs nor one another (CP_ERR_INVALID_ARG).
  * D 64 or 128 (CP_ERR_UNSUPPORTED otherwise, and for T > 16); B = 0 or T = 0 does
  * nothing. Enqueued on `stream` of the current device.
  */

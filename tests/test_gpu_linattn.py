@@ -361,3 +361,40 @@ def test_step_keeps_slow_decays_over_thousands_of_tokens():
         bound += 1.01 * norm(half_step) + 2.0 ** -24 * (norm(new) + 2.0 ** -24 * norm(ref))
     err = norm(one.double() - ref)
     assert torch.all(err <= bound), (err / bound).tolist()
+
+
+def test_outputs_over_one_another_are_refused():
+    """The same buffer as two outputs, or as an output and the workspace, also in part: several CTAs
+    would write its bytes in no order."""
+    plan = cp.Plan(1, 2, 4096, 64, 1, True, "contiguous")
+    n = 4096 * 2 * 64
+    rows = torch.zeros(4, n, dtype=torch.bfloat16, device="cuda")
+    q, k, v, do = (x.data_ptr() for x in rows)
+    ld, zs = torch.zeros(2, device="cuda"), torch.zeros(4, 1, 2, 64, 64, device="cuda")
+    z = [x.data_ptr() for x in zs]
+    buf = torch.zeros(4 * n + plan.linattn_workspace_bytes(), dtype=torch.bfloat16, device="cuda")
+    at = lambda i: buf.data_ptr() + 2 * i                    # element i
+    ws = at(4 * n)
+
+    def fwd(o=at(0), so=z[0], ws=ws):
+        return cp.lib().cp_linattn_fwd(plan.handle, q, k, v, ld.data_ptr(), z[1], o, so, ws, None)
+
+    def bwd(dq=at(0), dk=at(n), dv=at(2 * n), dsi=z[0], ws=ws):
+        return cp.lib().cp_linattn_bwd(plan.handle, q, k, v, ld.data_ptr(), do, z[1], z[2], dq, dk, dv, dsi, ws, None)
+    assert fwd() == 0 and bwd() == 0
+    for bad in (dict(o=z[0]), dict(so=at(n - 8)), dict(ws=at(0)), dict(ws=z[0]), dict(ws=z[1]), dict(o=ws + 64),
+                dict(ws=q), dict(so=ld.data_ptr())):
+        assert fwd(**bad) == -1, bad
+    for bad in (dict(dq=at(n)), dict(dk=at(2 * n)), dict(dv=at(0)), dict(dq=at(8)), dict(dv=at(n + 8)), dict(dsi=at(0)),
+                dict(ws=at(3 * n - 8)), dict(ws=z[2]), dict(dv=do + 16), dict(dsi=z[1] + 16)):
+        assert bwd(**bad) == -1, bad
+    assert fwd(o=at(n), so=None, ws=at(3 * n)) == 0 and bwd(dsi=None) == 0          # next to one another
+    s = [torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+
+    def step(o=s[3].data_ptr(), st=z[0]):
+        return cp.lib().cp_linattn_step(1, 1, 2, 64, *(x.data_ptr() for x in s[:3]), ld.data_ptr(), 0.1, st, o, None)
+    assert step() == 0
+    for bad in (dict(o=z[0]), dict(o=z[0] + 2 * 64 * 64 * 4 - 16), dict(st=s[0].data_ptr()), dict(o=ld.data_ptr())):
+        assert step(**bad) == -1, bad
+    torch.cuda.synchronize()
+    assert cp.check(plan) == 0
