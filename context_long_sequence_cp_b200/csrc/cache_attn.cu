@@ -711,6 +711,16 @@ int run_cache(cp_cache_plan_t plan, const void* q, const void* k, const void* v,
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return CP_ERR_CUDA;
   if (dev != plan->device) return CP_ERR_INVALID_ARG;
+  // Other CTAs read the cache, and the join reads the lengths again. Only the bf16 output may be
+  // the queries themselves: a CTA that writes rows has read them, and no other one does.
+  const size_t rows = static_cast<size_t>(plan->B) * plan->T * plan->Hq;
+  const size_t cache = sizeof(__nv_bfloat16) * plan->B * plan->cap * plan->Hkv * plan->D;
+  const size_t q_bytes = rows * plan->D * sizeof(__nv_bfloat16);
+  if (overlaps({{o, q_bytes}, {o_part, rows * plan->D * sizeof(float)}, {lse, rows * sizeof(float)},
+                {workspace, cache_workspace(*plan)}},
+               {{o == q ? nullptr : q, q_bytes}, {k, cache}, {v, cache}, {lengths, plan->B * sizeof(int32_t)},
+                {tree, static_cast<size_t>(plan->B) * plan->T * sizeof(int64_t)}}))
+    return CP_ERR_INVALID_ARG;
   CacheLaunch L;
   CacheParams& p = L.p;
   p.B = plan->B;

@@ -546,8 +546,9 @@ CP_API size_t cp_cache_attn_workspace_bytes(cp_cache_plan_t plan);
  *   o                : bf16 [B][T][Hq][D], device (written)
  *   lse              : float32 [B][Hq][T], device (written); may be NULL
  *   workspace        : device, cp_cache_attn_workspace_bytes(plan) bytes
- * Two kernels on `stream`; nothing is allocated; the values do not depend on timing. The
- * plan's device must be current (CP_ERR_INVALID_ARG). Waits that run out are reported by
+ * o may be q itself. Else outputs and the workspace must not overlap inputs nor one another
+ * (CP_ERR_INVALID_ARG). Two kernels on `stream`; nothing is allocated; the values do not depend
+ * on timing. The plan's device must be current (CP_ERR_INVALID_ARG). Waits that run out are reported by
  * cp_cache_check.
  */
 CP_API int cp_cache_attn(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache,

@@ -224,3 +224,47 @@ def test_same_as_the_fused_forward_on_a_full_context():
     # the fused forward keeps P in one bf16 term: its own tolerance
     assert torch.max(torch.abs(o_full[0, :, S - T:].float() - o.float())) <= 2e-2
     assert torch.max(torch.abs(lse_full[:, :, S - T:] - lse)) <= 1e-3
+
+
+def test_overlapping_buffers_are_refused():
+    """Outputs and the workspace over the cache, the lengths, the words, the queries or one another."""
+    B, T, Hq, Hkv, D, cap = 2, 3, 4, 2, 64, 300
+    q, k, v, n, words = (t.cuda() for t in case(B, T, Hq, Hkv, D, cap, (200, 297), seed=1))
+    plan = cp.CachePlan(B, Hq, Hkv, D, cap, T)
+    rows = B * T * Hq
+    o, lse = torch.empty(2 * rows * D, device="cuda"), torch.empty(rows, device="cuda")
+    ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    p = {name: t.data_ptr() for name, t in dict(q=q, k=k, v=v, n=n, words=words, o=o, lse=lse, ws=ws).items()}
+
+    def whole(**over):
+        a = {**p, **over}
+        return cp.lib().cp_cache_attn(plan.handle, a["q"], a["k"], a["v"], a["n"], a["words"], a["o"], a["lse"], a["ws"], None)
+
+    def part(**over):
+        a = {**p, **over}
+        return cp.lib().cp_cache_attn_partial(plan.handle, a["q"], a["k"], a["v"], a["n"], 1, a["words"], a["o"], a["lse"],
+                                              a["ws"], None)
+    end_k, end_v = p["k"] + 2 * k.numel(), p["v"] + 2 * v.numel()
+    for call in (whole, part):
+        assert call() == 0
+        for bad in (dict(o=p["k"]), dict(o=end_v - 16), dict(lse=end_k - 4), dict(ws=p["v"]), dict(ws=p["q"]),
+                    dict(o=p["n"]), dict(lse=p["n"]), dict(ws=p["words"]), dict(lse=p["o"] + 64), dict(o=p["ws"] + 1024),
+                    dict(lse=p["ws"]), dict(o=p["q"] + 16), dict(lse=p["q"])):
+            assert call(**bad) == -1, bad
+    assert part(o=p["q"]) == -1                                   # fp32 rows are twice as long
+    torch.cuda.synchronize()
+    assert cp.cache_check(plan) == 0
+
+
+@pytest.mark.parametrize("lengths", [(200, 297, 0), (8000, 3, 4000), (60, 61, 62)])
+def test_output_in_place_of_the_queries(lengths):
+    """Units whole in a CTA and cut among several, two query tiles per head: the same bits."""
+    B, T, Hq, Hkv, D = 3, 40, 8, 2, 128
+    q, k, v, n, words = (t.cuda() for t in case(B, T, Hq, Hkv, D, max(lengths) + T, lengths, seed=2))
+    plan = cp.CachePlan(B, Hq, Hkv, D, max(lengths) + T, T)
+    o, lse = cp.cache_attn(plan, q, k, v, n, words)
+    for _ in range(5):
+        mine = q.clone()
+        got, l2 = cp.cache_attn(plan, mine, k, v, n, words, o=mine)
+        assert got is mine and torch.equal(mine, o) and torch.equal(l2, lse)
+    assert cp.cache_check(plan) == 0
