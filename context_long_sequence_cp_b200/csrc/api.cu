@@ -1091,8 +1091,11 @@ int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* in, voi
   if (!aligned16(in) || !aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return CP_ERR_ALIGNMENT;
   const int rc = on_plan_device(plan);
   if (rc != CP_OK) return rc;
-  if (in == out) return CP_ERR_INVALID_ARG;   // a layout's rows move
   ra.axis_stride = static_cast<int64_t>(plan->B) * plan->S;
+  // A layout's rows move: one written in place could be read after that.
+  const size_t bytes = 2 * static_cast<size_t>(ra.axis_stride) * plan->H * D;
+  if (overlaps({{out, bytes}}, {{in, bytes}, {positions, sizeof(int32_t) * axes * ra.axis_stride}}))
+    return CP_ERR_INVALID_ARG;
   ra.inverse = direction;
   ra.half = pairing == CP_ROPE_PAIRS_HALF;
   return launch_rope_axes(permute_args(plan, direction, 2), ra, positions, in, out,

@@ -433,8 +433,9 @@ CP_API int cp_rope_permute(cp_attn_plan_t plan, const void* in, void* out, doubl
  *   positions : int32 [axes][B][S], device, any values, natural token order
  *   sections  : int [axes], host, each >= 1, their sum D/2 (CP_ERR_INVALID_ARG)
  * base > 1. Angles are reduced to [-pi, pi] in fp64, rotated in fp32, rounded to bf16
- * once. `in` and `out` must not overlap (the same pointer: CP_ERR_INVALID_ARG); both
- * 16-byte, positions 4-byte aligned (CP_ERR_ALIGNMENT). The plan's device must be current (CP_ERR_INVALID_ARG).
+ * once. `out` must not overlap `in` nor positions (CP_ERR_INVALID_ARG); `in` and `out` are
+ * 16-byte, positions 4-byte aligned (CP_ERR_ALIGNMENT). The plan's device must be current
+ * (CP_ERR_INVALID_ARG).
  */
 enum { CP_ROPE_FREQS_SHARED = 0, CP_ROPE_FREQS_PER_AXIS = 1 };
 enum { CP_ROPE_PAIRS_ADJACENT = 0, CP_ROPE_PAIRS_HALF = 1 };

@@ -5,6 +5,8 @@ Tolerance per element, from the arithmetic: the angle is reduced in fp64, its si
 cosine are fp32 (error below 1e-6 with the fp32 products), the result is rounded to bf16
 once, by at most half a step, 2^-8 of the value: |gpu - oracle| <= 2^-8 |oracle| + 1e-5 |pair|.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -115,3 +117,25 @@ def test_in_place_is_refused():
     pos = torch.zeros(1, 1, 64, dtype=torch.int32, device="cuda")
     with pytest.raises(cp.CpAttnError):
         cp.rope_axes(plan, x, pos, [32], out=x.view(1, 1, 64, 2, 64))
+
+
+def test_overlaps_are_refused():
+    """Rows move in the map: an output that begins inside the input, or over the positions."""
+    B, S, H, D = 2, 64, 2, 64
+    plan = cp.Plan(B, H, S, D, 2, True, "zigzag")
+    n = B * S * H * D
+    buf = torch.zeros(4 * n, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(2 * B * S + 2 * n, dtype=torch.int32, device="cuda")
+    sections = (ctypes.c_int * 2)(16, 16)
+
+    def call(x, y, inverse):
+        return cp.lib().cp_rope_axes_permute(plan.handle, inverse, x, y, pos.data_ptr(), 2, sections, 1e4, 0, 0, None)
+    at = lambda i: buf.data_ptr() + 2 * i
+    for inverse in (0, 1):
+        for x, y in ((at(0), at(n - 8)), (at(n - 8), at(0)), (at(8), at(0)), (at(0), at(0)), (at(0), pos.data_ptr()),
+                     (at(0), pos.data_ptr() + 4 * 2 * B * S - 16)):
+            assert call(x, y, inverse) == -1
+        assert call(at(0), at(n), inverse) == 0 and call(at(n), at(0), inverse) == 0
+        assert call(at(0), pos.data_ptr() + 4 * 2 * B * S, inverse) == 0
+    torch.cuda.synchronize()
+    assert cp.check(plan) == 0
