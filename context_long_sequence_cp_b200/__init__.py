@@ -566,10 +566,12 @@ def linattn_bwd(plan: Plan, q, k, v, log_decay, dout, state_in=None, dstate_out=
 
 def linattn_step(q, k, v, log_decay, state, scale: float = 0.0, o=None, stream=None):
     """``cp_linattn_step``: the recurrent form on T <= 16 new tokens, q, k, v bf16
-    [B, T, H, D]; ``state`` (fp32 [B, H, D, D]) is updated in place. scale 0 selects
-    1/sqrt(D). Returns o."""
+    [B, T, H, D]; log_decay fp32 [H], <= 0; ``state`` (fp32 [B, H, D, D]) is updated in
+    place. scale <= 0 selects 1/sqrt(D), as in ``Plan``. Returns o."""
     if q.dim() != 4:
         raise ValueError(f"q: expected [B, T, H, D], got {tuple(q.shape)}")
+    if not math.isfinite(scale):
+        raise ValueError(f"scale: expected a finite number, got {scale}")
     B, T, H, D = q.shape
     dev = q.device
     for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):

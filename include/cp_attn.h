@@ -502,6 +502,9 @@ CP_API size_t cp_linattn_workspace_bytes(cp_attn_plan_t plan);
  * exact to 2^-48; each token rounds the state to fp32 once, so what a decay nearer to 1
  * than 2^-25 (log_decay above -3e-8) takes off may be rounded away.
  *   q, k, v : bf16 [B][T][H][D], device;   o : the same (written)
+ *   log_decay : float32 [H], device, 4-byte aligned, <= 0 (-inf: no decayed state at all)
+ *   scale   : of o, any finite number as it is (CP_ERR_INVALID_ARG otherwise); 0 gives o = 0,
+ *             not the default that 0 selects for a plan
  *   state   : float32 [B][H][D][D], device, read and updated in place
  * o and state must not overlap the inputs nor one another (CP_ERR_INVALID_ARG).
  * D 64 or 128 (CP_ERR_UNSUPPORTED otherwise, and for T > 16); B = 0 or T = 0 does

@@ -190,3 +190,11 @@ def test_python_refuses_a_stream_of_another_device():
         cuda_stream, device = 0, torch.device("cuda", 1)
     with pytest.raises(ValueError, match="stream"):
         cp._enqueue(torch.device("cuda", 0), Stream(), lambda s: pytest.fail("launched"))
+
+
+@pytest.mark.parametrize("scale", [math.nan, math.inf, -math.inf])
+def test_python_refuses_a_scale_that_is_no_number(scale):
+    """As the library does; NaN is not one of the values that select the default."""
+    x, ld, st = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16), torch.zeros(2), torch.zeros(1, 2, 64, 64)
+    with pytest.raises(ValueError, match="scale"):
+        cp.linattn_step(x, x, x, ld, st, scale=scale)
