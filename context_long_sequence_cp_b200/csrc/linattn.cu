@@ -856,8 +856,9 @@ LinView lin_view(const PlanView& v) {
 // time in chunks of the output launch (3.1 us each): a wave costs its chunks, about 2.5 more
 // to fill and drain, and 0.35 for each earlier segment's state to join; a chunk of the state
 // launch 0.45. Measured on 148 SMs, us, the model's choice first: 32 heads of 256 chunks 4
-// segments 312, 3 394, 5 418, 9 322, 1 763; the backward of 4 heads of 256 chunks 12 133, 9 158,
-// 16 183, 1 767; 8 heads of 64 chunks 12 52.5, 16 50.8, 8 55.5, 1 202.
+// segments 309, 3 392, 5 418, 9 321, 1 759; 8 heads of 64 chunks 16 48.9, 12 52.1, 8 54.1, 18 51.7,
+// 1 195; their backward 6 71, 4 88, 8 96, 1 198; the backward of 4 heads of 256 chunks 12 130, 9 153,
+// 16 180, 1 763.
 constexpr int kMaxSegments = 64;
 int choose_segments(int64_t ctas, int64_t state_ctas, int nch, int sms) {
   int best = 1;

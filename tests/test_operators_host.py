@@ -198,3 +198,23 @@ def test_python_refuses_a_scale_that_is_no_number(scale):
     x, ld, st = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16), torch.zeros(2), torch.zeros(1, 2, 64, 64)
     with pytest.raises(ValueError, match="scale"):
         cp.linattn_step(x, x, x, ld, st, scale=scale)
+
+
+def test_linattn_segments_are_those_of_the_measured_comment():
+    """The rule that cuts a sequence into segments, restated, and its choices for the sizes whose
+    times stand beside it; the library's show in the bytes it asks for (the states of all segments
+    but the last, of one scan forward and of three backward)."""
+    def choose(ctas, state_ctas, chunks, sms=148):
+        def cost(s):
+            per = -(-chunks // s)
+            c = -(-ctas * s // sms) * (per + 2.5 + 0.35 * (s - 1))
+            return c + (-(-state_ctas * (s - 1) // sms) * (0.45 * per + 2.0) if s > 1 else 0.0)
+        return min(range(1, min(chunks, 64) + 1), key=cost)
+    assert choose(32, 32, 256) == 4 and choose(8, 8, 64) == 16 and choose(3 * 8, 2 * 8, 64) == 6
+    assert choose(3 * 4, 2 * 4, 256) == 12
+    if torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 148:
+        pytest.skip("the comment's figures are of 148 SMs")
+    for heads, chunks in ((32, 256), (8, 64), (4, 256), (16, 32), (1, 57), (300, 10)):
+        f, b = choose(heads, heads, chunks), choose(3 * heads, 2 * heads, chunks)
+        plan = cp.Plan(1, heads, chunks * 128, 64, 1, True, "contiguous")
+        assert plan.linattn_workspace_bytes() == max(f - 1, 3 * (b - 1)) * heads * 64 * 64 * 4
