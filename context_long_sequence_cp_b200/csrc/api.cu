@@ -111,8 +111,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // 4-D view (D, Hh, T, NR*B) of a bf16 tensor stored [NR*B][T][Hh][D]; box of
 // 64 x 1 x 128 x 1 elements (128 B x 128 rows) with the 128-byte swizzle.
 // A rank-local buffer holds B row blocks only (row_blocks = B).
@@ -703,7 +701,7 @@ int cp_attn_bwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v
   if (plan->g.T % 4 != 0) return CP_ERR_UNSUPPORTED;   // 16-byte rows of the per-row statistics
   const void* ptrs[11] = {q, k, v, o, lse, dout, dq, dk, dv, workspace, nullptr};
   for (int i = 0; i < 10; ++i)
-    if (!aligned16(ptrs[i])) return CP_ERR_ALIGNMENT;
+    if (!is_aligned16(ptrs[i])) return CP_ERR_ALIGNMENT;
   if (plan->d_items == nullptr || plan->bwd_kv.d_items == nullptr) return CP_ERR_CUDA;
   const Geometry& g = plan->g;
   const int64_t rows = static_cast<int64_t>(g.NR) * g.B * g.T * g.Hh;
@@ -775,8 +773,8 @@ size_t cp_attn_workspace_bytes(cp_attn_plan_t plan, int with_partials) {
 int cp_attn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, void* o, float* lse,
                 void* workspace, cp_stream_t stream) {
   if (plan == nullptr || q == nullptr || k == nullptr || v == nullptr || o == nullptr) return CP_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
-      !aligned16(workspace))
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(o) || !is_aligned16(lse) ||
+      !is_aligned16(workspace))
     return CP_ERR_ALIGNMENT;
   int rc = ensure_device(plan);
   if (rc != CP_OK) return rc;
@@ -807,7 +805,7 @@ int cp_attn_fwd_partials(cp_attn_plan_t plan, const void* q, const void* k, cons
       lse_parts == nullptr)
     return CP_ERR_INVALID_ARG;
   if (plan->layout == CP_LAYOUT_ULYSSES) return CP_ERR_UNSUPPORTED;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o_parts) || !aligned16(lse_parts))
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(o_parts) || !is_aligned16(lse_parts))
     return CP_ERR_ALIGNMENT;
   int rc = ensure_device(plan);
   if (rc != CP_OK) return rc;
@@ -885,7 +883,7 @@ int cp_attn_fwd_ring_step(cp_attn_plan_t plan, int rank, int step, const void* q
     return CP_ERR_INVALID_ARG;
   if (plan->layout == CP_LAYOUT_ULYSSES) return CP_ERR_UNSUPPORTED;
   if (rank < 0 || rank >= plan->N || step < 0 || step >= plan->N) return CP_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o_part) || !aligned16(lse_part))
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(o_part) || !is_aligned16(lse_part))
     return CP_ERR_ALIGNMENT;
   int rc = ensure_device(plan);
   if (rc != CP_OK) return rc;
@@ -944,7 +942,7 @@ int ring_launch(cp_attn_plan_t plan, int rank, const void* q, void* k_all, void*
   if (external && arrived == nullptr) return CP_ERR_INVALID_ARG;
   if (pull && plan->N > kMaxPullRanks) return CP_ERR_UNSUPPORTED;
   if (plan->N > 255) return CP_ERR_UNSUPPORTED;   // unit steps are packed in 8 bits
-  if (!aligned16(q) || !aligned16(k_all) || !aligned16(v_all) || !aligned16(o_parts) || !aligned16(lse_parts) ||
+  if (!is_aligned16(q) || !is_aligned16(k_all) || !is_aligned16(v_all) || !is_aligned16(o_parts) || !is_aligned16(lse_parts) ||
       (reinterpret_cast<uintptr_t>(arrived) & 3u))
     return CP_ERR_ALIGNMENT;
   const Geometry& g = plan->g;
@@ -956,7 +954,7 @@ int ring_launch(cp_attn_plan_t plan, int rank, const void* q, void* k_all, void*
     for (int j = 0; j < plan->N; ++j) {
       if (j == rank) continue;
       if (pull_k[j] == nullptr || pull_v[j] == nullptr) return CP_ERR_INVALID_ARG;
-      if (!aligned16(pull_k[j]) || !aligned16(pull_v[j])) return CP_ERR_ALIGNMENT;
+      if (!is_aligned16(pull_k[j]) || !is_aligned16(pull_v[j])) return CP_ERR_ALIGNMENT;
       P.pull_src[2 * j] = reinterpret_cast<uint64_t>(pull_k[j]);
       P.pull_src[2 * j + 1] = reinterpret_cast<uint64_t>(pull_v[j]);
     }
@@ -1023,7 +1021,7 @@ int cp_merge_partials(int num_parts, int64_t rows, int D, const float* o_parts, 
   if (num_parts < 1 || num_parts > 64 || rows < 0) return CP_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return CP_ERR_UNSUPPORTED;
   if (rows > 0 && (o_parts == nullptr || lse_parts == nullptr || o_out == nullptr)) return CP_ERR_INVALID_ARG;
-  if (!aligned16(o_parts) || !aligned16(o_out) || (reinterpret_cast<uintptr_t>(lse_parts) & 3u) ||
+  if (!is_aligned16(o_parts) || !is_aligned16(o_out) || (reinterpret_cast<uintptr_t>(lse_parts) & 3u) ||
       (reinterpret_cast<uintptr_t>(lse_out) & 3u))
     return CP_ERR_ALIGNMENT;
   return launch_merge(num_parts, rows, D, o_parts, lse_parts, static_cast<__nv_bfloat16*>(o_out), lse_out,
@@ -1037,7 +1035,7 @@ int cp_layout_permute(cp_attn_plan_t plan, int direction, const void* in, void* 
   if (plan == nullptr || in == nullptr || out == nullptr) return CP_ERR_INVALID_ARG;
   if (direction != 0 && direction != 1) return CP_ERR_INVALID_ARG;
   if (elem_bytes != 2 && elem_bytes != 4) return CP_ERR_INVALID_ARG;
-  if (!aligned16(in) || !aligned16(out)) return CP_ERR_ALIGNMENT;
+  if (!is_aligned16(in) || !is_aligned16(out)) return CP_ERR_ALIGNMENT;
   const PermuteArgs a = permute_args(plan, direction, elem_bytes);
   const int64_t unit_elems =
       a.kind == 0 ? static_cast<int64_t>(plan->H) * plan->D : static_cast<int64_t>(plan->H / plan->N) * plan->D;
@@ -1052,7 +1050,7 @@ int cp_rope_permute(cp_attn_plan_t plan, const void* in, void* out, double base,
   if (plan == nullptr || in == nullptr || out == nullptr) return CP_ERR_INVALID_ARG;
   if (!(base > 1.0) || !std::isfinite(base)) return CP_ERR_INVALID_ARG;
   if (pos_offset < 0 || pos_offset > (int64_t(1) << 31) - plan->S) return CP_ERR_INVALID_ARG;
-  if (!aligned16(in) || !aligned16(out)) return CP_ERR_ALIGNMENT;
+  if (!is_aligned16(in) || !is_aligned16(out)) return CP_ERR_ALIGNMENT;
   if (plan->D % 8 != 0 || plan->D > 128 || 256 % plan->D != 0) return CP_ERR_UNSUPPORTED;
   int ndev = 0;
   if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) return CP_ERR_CUDA;
@@ -1088,7 +1086,7 @@ int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* in, voi
     }
   }
   if (pair != D / 2) return CP_ERR_INVALID_ARG;
-  if (!aligned16(in) || !aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return CP_ERR_ALIGNMENT;
+  if (!is_aligned16(in) || !is_aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return CP_ERR_ALIGNMENT;
   const int rc = on_plan_device(plan);
   if (rc != CP_OK) return rc;
   ra.axis_stride = static_cast<int64_t>(plan->B) * plan->S;
@@ -1114,9 +1112,9 @@ int cp_sp_rs_dropout_add_ln(const void* partials, int nparts, int64_t rows, int 
   if (y_out != nullptr && gamma == nullptr) return CP_ERR_INVALID_ARG;
   if (z_out == nullptr && y_out == nullptr) return CP_ERR_INVALID_ARG;
   if (y_out != nullptr && !(eps > 0.f)) return CP_ERR_INVALID_ARG;
-  if (!aligned16(partials) || (residual != nullptr && !aligned16(residual)) || (gamma != nullptr && !aligned16(gamma)) ||
-      (beta != nullptr && !aligned16(beta)) || (z_out != nullptr && !aligned16(z_out)) ||
-      (y_out != nullptr && !aligned16(y_out)) ||
+  if (!is_aligned16(partials) || (residual != nullptr && !is_aligned16(residual)) || (gamma != nullptr && !is_aligned16(gamma)) ||
+      (beta != nullptr && !is_aligned16(beta)) || (z_out != nullptr && !is_aligned16(z_out)) ||
+      (y_out != nullptr && !is_aligned16(y_out)) ||
       (keep_bits != nullptr && (reinterpret_cast<uintptr_t>(keep_bits) & 3u) != 0))
     return CP_ERR_ALIGNMENT;
   int ndev = 0;
@@ -1146,7 +1144,7 @@ int64_t cp_layout_index_map_len(cp_attn_plan_t plan) {
 
 int cp_layout_index_map(cp_attn_plan_t plan, int64_t* map_out, cp_stream_t stream) {
   if (plan == nullptr || map_out == nullptr) return CP_ERR_INVALID_ARG;
-  if (!aligned16(map_out)) return CP_ERR_ALIGNMENT;
+  if (!is_aligned16(map_out)) return CP_ERR_ALIGNMENT;
   int ndev = 0;
   if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) return CP_ERR_CUDA;
   return launch_index_map(permute_args(plan, 0, 2), map_out, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -1200,7 +1198,7 @@ int cp_internal_ulysses_fwd_scratch(cp_attn_plan_s* plan, const void* q, const v
                                     float* lse, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   if (plan == nullptr || q == nullptr || k == nullptr || v == nullptr || o == nullptr) return CP_ERR_INVALID_ARG;
   if (plan->layout != CP_LAYOUT_ULYSSES) return CP_ERR_UNSUPPORTED;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(scratch))
+  if (!is_aligned16(q) || !is_aligned16(k) || !is_aligned16(v) || !is_aligned16(o) || !is_aligned16(lse) || !is_aligned16(scratch))
     return CP_ERR_ALIGNMENT;
   const size_t tensor = static_cast<size_t>(plan->B) * plan->S * plan->H * plan->D * 2;
   if (scratch == nullptr || scratch_bytes < 4 * tensor) return CP_ERR_WORKSPACE;
