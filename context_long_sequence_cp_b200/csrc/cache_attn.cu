@@ -2,12 +2,15 @@
 // cache (sm_100a, tcgen05 + TMEM + TMA): single tokens when decoding, chains or trees of
 // drafted tokens when several are checked at once.
 //
-// The rows of a product are the (token, query head) pairs that share a key/value head,
-// so a cache row is read once for all of them. Token t sees the cached keys
+// The rows of a product are the (token, query head) pairs that share a key/value head, up
+// to 128 of them (a query tile: whole tokens of G = Hq / Hkv rows each), so a cache row is
+// read once for each query tile: once in all where T <= floor(128 / G). Token t sees the cached keys
 // [0, lengths[b]) and, among the drafted ones (cache rows lengths[b] + u), those whose
 // bit u is set in its tree word. Softmax, lse and partials are those of attn_fwd.cu.
 //
-// Bound: HBM, the cache read once (4 D bytes per key and key/value head). The 128-key
+// Bound: HBM, the cache read once per query tile (4 D bytes per key and key/value head; the
+// later tiles of a head come at other times, so what they share in L2 is chance: 65536 keys,
+// 4 key/value heads of 16 query heads, 64 tokens in eight tiles 200 us, 8 tokens in one 53). The 128-key
 // tiles of all (sequence, head, query tile) units are laid end to end and cut into equal
 // runs, one per CTA (one CTA per SM), so uneven lengths leave no SM idle. A run that
 // covers a unit whole writes its output; pieces of a unit go to fp32 slots, two per CTA,
@@ -15,12 +18,14 @@
 // the even and the odd key tiles, each with its own maximum, sum and accumulator (joined
 // at the unit's end), so that one's softmax runs under the other's products.
 //
-// Measured, 131040 cached keys, 8 key/value heads of 4 query heads, D = 128: 32 drafted
-// tokens 108 us, of them 97 in the first kernel (5.5 TB/s, 0.85 of the copy rate) and 9 in the
-// join, which can start only when the last CTA is done; one token 92 us. Sixteen sequences of
-// 0 to 8176 keys, 16 drafted tokens each: 66 us, 4.1 TB/s: about two units per CTA, whose start and end are not
-// hidden under another's products. P is kept to 2^-17 in two bf16 terms, so that a row of a
-// partial is as exact as its fp32 type says.
+// Measured, 131040 cached keys, 8 key/value heads of 4 query heads, D = 128, at an SM clock of
+// 1965 MHz: 32 drafted tokens 108 us, of them 97 in the first kernel (5.5 TB/s, 0.85 of the copy
+// rate) and 9 in the join, which starts when the last CTA is done; one token 94 us. Run without
+// a pause the card reaches its power limit and the clock falls to 1490 MHz: 127 to 140 us
+// and 112, so there the softmax's chain per tile bounds it and not HBM. Sixteen sequences of 0
+// to 8176 keys, 16 drafted tokens each: 63 us, 4.3 TB/s (73 at 1730 MHz): about two units per
+// CTA, whose start and end are not hidden under another's products. P is kept to 2^-17 in two
+// bf16 terms, so that a row of a partial is as exact as its fp32 type says.
 //
 // Cache rows that no token sees, past the last key or a tree's padding, are never read as
 // values: their scores are set to -inf and their rows of V are cleared in shared memory, so

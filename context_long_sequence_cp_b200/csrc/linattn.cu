@@ -25,9 +25,11 @@
 // joins those before it at its start.
 //
 // Bound. The forward cannot do without 8 bytes per element (164 us for 32768 tokens, 32 heads,
-// D = 128, at the card's copy rate); the two launches read B and C twice. Measured there:
-// 320 us, 75 of them for the segments' states, and 363 (125 and 237) where a last state is
-// asked for; with loads that all hit L2 302, so HBM is not what bounds it. A chunk takes
+// D = 128, at the card's copy rate); the two launches read B and C twice. Measured there, at an
+// SM clock of 1965 MHz: 308 us, a quarter of them for the segments' states, and 351 (a third) where
+// a last state is asked for; run without a pause, where the card's power limit holds the clock at
+// 1640 to 1665 MHz, 363 and 413. With loads that all hit L2 302 instead of 320, so HBM is not what
+// bounds it; the time follows the clock. A chunk takes
 // ~5600 cycles of an SM, the tensor core ~2400 of them: the chain of the state's warps
 // (weight C, the product, add, publish Z) and that of the score warps (scores, P, the
 // product, output) meet once per chunk, and each is about that long. Not kept, measured:

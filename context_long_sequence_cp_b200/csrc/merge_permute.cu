@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) rope_permute_kernel(UnitMap m, int64_t un
 // cosines and sines they need by shuffles, so an angle is computed once per unit
 // and not once per head group. A lane always meets the same pairs: the stride
 // LPU is a multiple of the lanes that span a head. Measured on 32768 tokens of 32
-// heads, D = 128, three axes: 88 us, 6.1 TB/s, 0.93 of the copy rate. Few tokens
+// heads, D = 128, three axes: 91 us, 5.9 TB/s, 0.90 of the copy rate. Few tokens
 // are bound by the launch (6 us for 2 to 2000).
 template <int D, int LPU, bool HALF>
 __global__ void __launch_bounds__(256) rope_axes_kernel(UnitMap m, int64_t units, int vec_per_unit,

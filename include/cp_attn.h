@@ -37,7 +37,8 @@
  *   - Device pointers must be 16-byte aligned (CP_ERR_ALIGNMENT otherwise).
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream). Entry points
  *     that take a stream only enqueue work: they neither allocate device memory
- *     nor synchronise, except cp_attn_check, which synchronises `stream`.
+ *     nor synchronise, except cp_attn_check and cp_cache_check, which synchronise
+ *     `stream`.
  *   - The caller owns every input, output and workspace buffer. A plan owns only
  *     its host schedule and a small device table (work list + status word)
  *     allocated by cp_attn_plan and freed by cp_attn_plan_destroy.
@@ -463,11 +464,15 @@ CP_API int cp_rope_axes_permute(cp_attn_plan_t plan, int direction, const void* 
  *   workspace : device, cp_linattn_workspace_bytes(plan) bytes (NULL if 0)
  * The state is held and summed in fp32; the decayed scores and the state that the
  * queries read are rounded to bf16 once, as tensor-core operands. Values must be
- * finite: within a chunk of 128 tokens a NaN or infinity also reaches the tokens before
- * it. Outputs and the workspace must not overlap inputs nor one another (CP_ERR_INVALID_ARG);
- * calls that may overlap on the GPU need outputs and workspaces of their own. One or
- * two kernels; nothing is allocated; results do not depend on timing. Waits that run
- * out are reported by cp_attn_check. The plan's device must be current
+ * finite: a NaN or infinity also reaches tokens before it, those of its chunk of 128
+ * and, in a zigzag plan whose pieces (S / 2N tokens) are no multiple of 128, the last
+ * ones of the rank's other piece and whatever comes after them. For decays above
+ * e^-0.375 the scores are held times up to e^48, so products of a score and a row above
+ * 4e17 overflow. S is limited as the plan's: fewer than 2^13 tiles of 128 tokens.
+ * Outputs and the workspace must not overlap inputs nor one another
+ * (CP_ERR_INVALID_ARG); calls that may overlap on the GPU need outputs and workspaces of
+ * their own. One or two kernels; nothing is allocated; results do not depend on timing.
+ * Waits that run out are reported by cp_attn_check. The plan's device must be current
  * (CP_ERR_INVALID_ARG).
  */
 CP_API int cp_linattn_fwd(cp_attn_plan_t plan, const void* q, const void* k, const void* v, const float* log_decay,
@@ -552,8 +557,8 @@ CP_API size_t cp_cache_attn_workspace_bytes(cp_cache_plan_t plan);
  *   workspace        : device, cp_cache_attn_workspace_bytes(plan) bytes
  * o may be q itself. Else outputs and the workspace must not overlap inputs nor one another
  * (CP_ERR_INVALID_ARG). Two kernels on `stream`; nothing is allocated; the values do not depend
- * on timing. The plan's device must be current (CP_ERR_INVALID_ARG). Waits that run out are reported by
- * cp_cache_check.
+ * on timing. The plan's device must be current (CP_ERR_INVALID_ARG). Waits that run out are
+ * reported by cp_cache_check.
  */
 CP_API int cp_cache_attn(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* lengths, const int64_t* tree, void* o, float* lse, void* workspace,
@@ -564,7 +569,7 @@ CP_API int cp_cache_attn(cp_cache_plan_t plan, const void* q, const void* k_cach
  * them, for cp_merge_partials: o_part float32 [B*T*Hq][D] (normalised), lse_part float32
  * [B*T*Hq], row (b*T + t)*Hq + h. own_drafts = 1: the T drafted rows follow this rank's
  * lengths[b] rows, as above; 0: another rank holds them (lengths[b] <= capacity, tree
- * unused).
+ * unused). No output may overlap an input.
  */
 CP_API int cp_cache_attn_partial(cp_cache_plan_t plan, const void* q, const void* k_cache, const void* v_cache,
                                  const int32_t* lengths, int own_drafts, const int64_t* tree, float* o_part,
