@@ -746,8 +746,8 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const LinStepParams p
     sm.qk[t][d] = make_float2(__bfloat162float(p.q[at]) * p.scale, __bfloat162float(p.k[at]));
     if (d < CW) sm.v[t][d] = __bfloat162float(p.v[at + sl * CW]);
   }
-  // d as an fp32 pair, as in the chunked form: one fp32 number is off by up to 2^-25 of it, the same
-  // way at every call, and a state kept over thousands of tokens would show that.
+  // d as an fp32 pair, as in the chunked form: one fp32 exponential is off by up to 2^-23 of it, the
+  // same way at every call, and a state kept over thousands of tokens would show that.
   const double d = decay_pow(static_cast<double>(__ldg(p.log_decay + h)), 1);
   const float hi = static_cast<float>(d), lo = static_cast<float>(d - static_cast<double>(hi));
   const uint64_t hi2 = f2_pack(hi, hi), lo2 = f2_pack(lo, lo);
